@@ -201,8 +201,10 @@ pararnn_status pararnn_newton_backward(pararnn_cell cell, int64_t B, int64_t T, 
 
 /* Waits for `stream` and returns what the GPU recorded for the last forward
  * or backward call that used `workspace`: PARARNN_OK, PARARNN_ENONFINITE or
- * PARARNN_ETIMEOUT (ETIMEOUT wins if both happened); PARARNN_ECUDA if the copy
- * or the synchronisation fails. */
+ * PARARNN_ETIMEOUT (ETIMEOUT wins if both happened), or PARARNN_EINVAL for an
+ * index in device memory that was out of range (pararnn_gated_scan_step's
+ * slots; it wins over ENONFINITE); PARARNN_ECUDA if the copy or the
+ * synchronisation fails. */
 pararnn_status pararnn_status_sync(const void* workspace, void* stream);
 
 /* Static, NUL-terminated name of a status code ("PARARNN_OK", ...). */
@@ -446,6 +448,122 @@ pararnn_status pararnn_head_gru_backward(int64_t B, int64_t T, int64_t D, int n_
 pararnn_status pararnn_head_gru_unroll(int64_t B, int64_t T, int64_t D, int n_heads, pararnn_dtype px_dtype,
                                        const void* preacts, const float* U, const float* h0, float* H_out,
                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- gated linear recurrence ----------------------------------------------
+ * An affine diagonal recurrence with its gates inside (pararnn-torch page, News
+ * section: a recurrence that is affine in the state needs one exact scan and no
+ * Newton iteration; "Were RNNs all we needed?" thread: gates that do not depend
+ * on the state).  With c = decay > 0 and, per channel d,
+ *     r = sig(p_r),  i = sig(p_i),  y = c softplus(lambda_d) r,  a = e^-y,
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,     h_{-1} = h0.
+ * A step that `reset` marks starts from a zero state: h_t has no term in
+ * h_{t-1}, whatever h_{t-1} is, a NaN or Inf included.  Marking the first steps
+ * of sequences laid one behind the other keeps them apart.
+ *
+ * Layouts (row-major, channels fastest, device memory owned by the caller):
+ *   preacts    (B, T, 3, D)  dtype (float32 or bfloat16): p_r, p_i, x
+ *   lambda     (D)           float32
+ *   h0         (B, D)        float32, or NULL for a zero initial state
+ *   reset      (B, T)        bytes, non-zero marks; or NULL for none
+ *   H          (B, T, D)     dtype: the states, rounded once
+ *   h_last     (B, D)        float32: h_{T-1} unrounded (h0, or zero, when T is 0);
+ *                            may be h0's own buffer; or NULL
+ *   checkpoints              pararnn_gated_scan_checkpoint_bytes(...) bytes,
+ *                            4-byte aligned: states that the backward pass starts
+ *                            from, in a layout private to the library; or NULL
+ * State, gates and scan are float32.  Apart from h_last and h0, an output that
+ * overlaps an input or another output is not supported.  B*T must be below 2^31.
+ *
+ * workspace    NULL, and device-detected conditions are not recorded; or at least
+ *              256 bytes, 16-byte aligned, any contents, for
+ *              pararnn_status_sync(), which reports a NaN or Inf in H or h_last as
+ *              PARARNN_ENONFINITE.
+ * Errors: PARARNN_EINVAL, with nothing launched, for bad sizes, dtype or decay and
+ * for null, host or misaligned pointers; PARARNN_ECUDA if a launch fails. */
+size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype);
+pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
+                                          const float* lambda, float decay, const float* h0, const uint8_t* reset,
+                                          void* H_out, float* h_last, float* checkpoints, void* workspace,
+                                          size_t ws_bytes, void* stream);
+
+/* Its adjoint, from the checkpoints of a forward call with the same preacts,
+ * lambda, decay, h0 and reset.  With g = dL/dH, l_t = g_t + a_{t+1} l_{t+1} (no
+ * second term where step t+1 is marked), l_{T-1} = g_{T-1} + dL/dh_last:
+ *     dL/dx   = l b i                        (b = sqrt(1 - a^2))
+ *     dL/dp_i = l b i x (1 - i)
+ *     dL/dp_r = w (1 - r),  w = y l (a^2 i x / b - a h_{t-1})
+ *     dL/dlambda = sig(lambda) / softplus(lambda) * sum over b, t of w
+ *     dL/dh0  = a_0 l_0  (zero where step 0 is marked)
+ * The sums run in float32 in an order that the sizes and the device fix, with no
+ * floating-point atomics: repeated calls give identical bits.
+ *   dL_dH       (B, T, D)     dtype
+ *   dL_dh_last  (B, D)        float32, or NULL for zeros
+ *   dL_dpx      (B, T, 3, D)  dtype, written
+ *   dL_dlambda  (D)           float32, written; or NULL
+ *   dL_dh0      (B, D)        float32, written; or NULL
+ *   workspace   >= pararnn_gated_scan_workspace_bytes(B, T, D) bytes, 16-byte
+ *               aligned, any contents
+ * Errors as for the forward; a NaN or Inf in dL_dpx is recorded for
+ * pararnn_status_sync(). */
+size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D);
+pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
+                                           const float* lambda, float decay, const uint8_t* reset,
+                                           const float* checkpoints, const void* dL_dH, const float* dL_dh_last,
+                                           void* dL_dpx, float* dL_dlambda, float* dL_dh0, void* workspace,
+                                           size_t ws_bytes, void* stream);
+
+/* One token for each of N rows, on a cache of states that is updated in place
+ * (pararnn-torch page, API overview: decode_step, the one-step recurrence):
+ *     state[slots[n]] = a h + b i x with h = state[slots[n]];  y[n] = that state
+ *   preacts  (N, 3, D) dtype;  y (N, D) dtype, written
+ *   slots    (N) int32, or NULL for slot n of row n (N <= n_slots)
+ *   state    (n_slots, D) float32, read and written
+ * A row whose slot is negative is padding: its y is left as it was.  Rows that
+ * name the same slot are taken in the order of their rows, each on the state that
+ * the one before left.  A slot at or above n_slots is an error that the GPU
+ * finds: the row is skipped as if it were padding, and pararnn_status_sync()
+ * reports PARARNN_EINVAL if the call had a workspace.  Workspace and errors
+ * otherwise as for the forward. */
+pararnn_status pararnn_gated_scan_step(int64_t N, int64_t D, pararnn_dtype dtype, const void* preacts,
+                                       const float* lambda, float decay, int64_t n_slots, const int32_t* slots,
+                                       float* state, void* y, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- layer normalisation ---------------------------------------------------
+ * x is (M, P, N): each row of N values is normalised by itself, and row (m, p)
+ * is scaled and shifted by weight[p] and bias[p]:
+ *     xh = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = xh weight + bias
+ * with var the mean of (x - mean)^2.  P = 1 is layer normalisation over the
+ * channels; pre-activations (B, T, G, D) are M = B*T, P = G, N = D, a scale and a
+ * shift for each gate, laid out like diag_w; a state (B, T, D) of n_heads heads
+ * is M = B*T, P = n_heads, N = D / n_heads.  (The ParaRNN pages have no
+ * counterpart: it is the normalisation around a recurrent layer.)
+ *   x, y          (M, P, N)  dtype (float32 or bfloat16); y may be x's buffer
+ *   weight, bias  (P, N)     float32, or NULL for ones, zeros
+ *   eps           finite, >= 0.  A constant row with eps = 0 gives NaN (0 times
+ *                 Inf)
+ *   mean, rstd    (M, P)     float32, written; or NULL
+ * P and N are at least 1; M*P and P*N must be below 2^31.  Sums are float32.
+ * Workspace (NULL or 256 bytes) and errors as for pararnn_gated_scan_forward. */
+pararnn_status pararnn_layer_norm_forward(int64_t M, int64_t P, int64_t N, pararnn_dtype dtype, const void* x,
+                                          const float* weight, const float* bias, float eps, void* y, float* mean,
+                                          float* rstd, void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradients, from the forward's mean and rstd.  With d = dL/dy weight:
+ *     dL/dx = rstd (d - mean(d) - xh mean(d xh))
+ *     dL/dweight[p] = sum over m of dL/dy xh,  dL/dbias[p] = sum over m of dL/dy
+ * The sums over m run in float32 in an order that the sizes and the device fix:
+ * repeated calls give identical bits.
+ *   dL_dy       (M, P, N) dtype;  dL_dx (M, P, N) dtype, written, may be dL_dy's
+ *               or x's buffer
+ *   dL_dweight, dL_dbias  (P, N) float32, written; or NULL
+ *   workspace   >= pararnn_layer_norm_workspace_bytes(M, P, N) bytes, 16-byte
+ *               aligned, any contents
+ * A NaN or Inf in dL_dx is recorded for pararnn_status_sync(). */
+size_t pararnn_layer_norm_workspace_bytes(int64_t M, int64_t P, int64_t N);
+pararnn_status pararnn_layer_norm_backward(int64_t M, int64_t P, int64_t N, pararnn_dtype dtype, const void* x,
+                                           const float* weight, const float* mean, const float* rstd,
+                                           const void* dL_dy, void* dL_dx, float* dL_dweight, float* dL_dbias,
+                                           void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,7 @@ OK, EINVAL, ENONFINITE, ETIMEOUT, ECUDA = 0, 1, 2, 3, 4
 
 # every exported symbol of include/pararnn_b200.h, with its C signature
 _P, _I64, _I, _SZ, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+_F = ctypes.c_float
 SIGNATURES = {
     "pararnn_num_gates": (_I, [_I]),
     "pararnn_state_width": (_I, [_I]),
@@ -50,6 +51,14 @@ SIGNATURES = {
     "pararnn_head_gru_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
     "pararnn_head_gru_backward": (_I, [_I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "pararnn_head_gru_unroll": (_I, [_I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pararnn_gated_scan_checkpoint_bytes": (_SZ, [_I64, _I64, _I64, _I]),
+    "pararnn_gated_scan_forward": (_I, [_I64, _I64, _I64, _I, _P, _P, _F, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pararnn_gated_scan_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "pararnn_gated_scan_backward": (_I, [_I64, _I64, _I64, _I, _P, _P, _F, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pararnn_gated_scan_step": (_I, [_I64, _I64, _I, _P, _P, _F, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "pararnn_layer_norm_forward": (_I, [_I64, _I64, _I64, _I, _P, _P, _P, _F, _P, _P, _P, _P, _SZ, _P]),
+    "pararnn_layer_norm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "pararnn_layer_norm_backward": (_I, [_I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -215,6 +224,49 @@ def pararnn_head_gru_backward(B, T, D, n_heads, px_dtype, preacts, U, h0, H, dL_
 def pararnn_head_gru_unroll(B, T, D, n_heads, px_dtype, preacts, U, h0, H_out, workspace, ws_bytes, stream):
     return load().pararnn_head_gru_unroll(B, T, D, n_heads, px_dtype, _ptr(preacts), _ptr(U), _ptr(h0), _ptr(H_out),
                                           _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def pararnn_gated_scan_checkpoint_bytes(B, T, D, dtype):
+    return load().pararnn_gated_scan_checkpoint_bytes(B, T, D, dtype)
+
+
+def pararnn_gated_scan_forward(B, T, D, dtype, preacts, lam, decay, h0, reset, H_out, h_last, checkpoints, workspace,
+                               ws_bytes, stream):
+    return load().pararnn_gated_scan_forward(B, T, D, dtype, _ptr(preacts), _ptr(lam), decay, _ptr(h0), _ptr(reset),
+                                             _ptr(H_out), _ptr(h_last), _ptr(checkpoints), _ptr(workspace), ws_bytes,
+                                             _stream(stream))
+
+
+def pararnn_gated_scan_workspace_bytes(B, T, D):
+    return load().pararnn_gated_scan_workspace_bytes(B, T, D)
+
+
+def pararnn_gated_scan_backward(B, T, D, dtype, preacts, lam, decay, reset, checkpoints, dL_dH, dL_dh_last, dL_dpx,
+                                dL_dlam, dL_dh0, workspace, ws_bytes, stream):
+    return load().pararnn_gated_scan_backward(B, T, D, dtype, _ptr(preacts), _ptr(lam), decay, _ptr(reset),
+                                              _ptr(checkpoints), _ptr(dL_dH), _ptr(dL_dh_last), _ptr(dL_dpx),
+                                              _ptr(dL_dlam), _ptr(dL_dh0), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def pararnn_gated_scan_step(N, D, dtype, preacts, lam, decay, n_slots, slots, state, y, workspace, ws_bytes, stream):
+    return load().pararnn_gated_scan_step(N, D, dtype, _ptr(preacts), _ptr(lam), decay, n_slots, _ptr(slots),
+                                          _ptr(state), _ptr(y), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def pararnn_layer_norm_forward(M, P, N, dtype, x, weight, bias, eps, y, mean, rstd, workspace, ws_bytes, stream):
+    return load().pararnn_layer_norm_forward(M, P, N, dtype, _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y),
+                                             _ptr(mean), _ptr(rstd), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def pararnn_layer_norm_workspace_bytes(M, P, N):
+    return load().pararnn_layer_norm_workspace_bytes(M, P, N)
+
+
+def pararnn_layer_norm_backward(M, P, N, dtype, x, weight, mean, rstd, dL_dy, dL_dx, dL_dweight, dL_dbias, workspace,
+                                ws_bytes, stream):
+    return load().pararnn_layer_norm_backward(M, P, N, dtype, _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                              _ptr(dL_dy), _ptr(dL_dx), _ptr(dL_dweight), _ptr(dL_dbias),
+                                              _ptr(workspace), ws_bytes, _stream(stream))
 
 
 # ---- tensor-level helpers (allocation through torch, compute in the library) ----
@@ -444,3 +496,249 @@ def newton_step_host(cell, px_host, dL_dH_host, diag_w=None, h0=None, K=1, chann
     if sync_status:
         _check(pararnn_status_sync(workspace, st), "pararnn_newton_step_host (device status)")
     return H_host, dpx_host, da
+
+
+# ---- gated linear recurrence and layer normalisation ------------------------
+
+def _same_device(px, *tensors):
+    """Every given tensor is contiguous and on px's CUDA device."""
+    if px.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, got %s" % px.device)
+    for t in (px,) + tensors:
+        if t is None:
+            continue
+        if t.device != px.device:
+            raise ValueError("tensors on different devices: %s and %s" % (px.device, t.device))
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous, got strides %s" % (t.stride(),))
+
+
+def _expect(name, t, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError("%s must be %s %s, got %s %s" % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+
+
+def _launch(call, px, stream, scratch):
+    """Runs call(stream) with px's device current.  Memory in `scratch` was
+    allocated here on torch's current stream: when the call runs on another
+    stream, the allocator is told, so that it is not handed out again before
+    that stream is done with it."""
+    import torch
+
+    with torch.cuda.device(px.device):
+        cur = torch.cuda.current_stream(px.device)
+        st = stream if stream is not None else cur
+        handle = _stream(st)
+        if handle != cur.cuda_stream:
+            ext = st if not isinstance(st, int) else torch.cuda.ExternalStream(st, device=px.device)
+            ext.wait_stream(cur)  # the memory may still be in use by earlier work of the stream it came from
+            for t in scratch:
+                if t is not None:
+                    t.record_stream(ext)
+        return call(handle)
+
+
+def _status(workspace, px, stream, where):
+    import torch
+
+    with torch.cuda.device(px.device):
+        st = stream if stream is not None else torch.cuda.current_stream(px.device)
+        _check(pararnn_status_sync(workspace, st), where + " (device status)")
+
+
+def _header(workspace, sync_status, device):
+    """The workspace of a call that needs one only to record its status."""
+    import torch
+
+    if workspace is None and sync_status:
+        return torch.empty(256, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _scan_shape(px, lam, ndim):
+    import torch
+
+    if px.dim() != ndim or px.shape[-2] != 3:
+        raise ValueError("preacts must be (%s3, D), got %s" % ("B, T, " if ndim == 4 else "N, ", tuple(px.shape)))
+    _expect("lam", lam, (px.shape[-1],), torch.float32)
+    return _dtype_code(px)
+
+
+def _mask(reset, B, T):
+    import torch
+
+    if reset is None:
+        return None
+    if reset.dtype == torch.bool:
+        reset = reset.view(torch.uint8)
+    _expect("reset", reset, (B, T), torch.uint8)
+    return reset
+
+
+def gated_scan_forward(px, lam, decay=8.0, h0=None, reset=None, want_grad=False, out=None, h_last=None,
+                       workspace=None, stream=None, sync_status=True):
+    """The gated linear recurrence: px (B,T,3,D) float32 or bfloat16, lam (D),
+    h0 (B,D) or None, reset (B,T) bool or uint8 or None (steps that start from
+    a zero state).  Returns (H (B,T,D) in px's dtype, the last state (B,D)
+    float32, the checkpoints that gated_scan_backward takes, or None without
+    want_grad).  With sync_status=False the call does not wait, and records
+    its status only in a workspace (>= 256 bytes) that is passed."""
+    import torch
+
+    code = _scan_shape(px, lam, 4)
+    B, T, _, D = px.shape
+    reset = _mask(reset, B, T)
+    _expect("h0", h0, (B, D), torch.float32)
+    _expect("out", out, (B, T, D), px.dtype)
+    _expect("h_last", h_last, (B, D), torch.float32)
+    _same_device(px, lam, h0, reset, out, h_last, workspace)
+    H = torch.empty((B, T, D), dtype=px.dtype, device=px.device) if out is None else out
+    last = torch.empty((B, D), dtype=torch.float32, device=px.device) if h_last is None else h_last
+    ck = None
+    if want_grad:
+        n = pararnn_gated_scan_checkpoint_bytes(B, T, D, code)
+        ck = torch.empty(n // 4, dtype=torch.float32, device=px.device)
+    ws = _header(workspace, sync_status, px.device)
+    _check(_launch(lambda st: pararnn_gated_scan_forward(B, T, D, code, px, lam, decay, h0, reset, H, last, ck, ws,
+                                                         ws.numel() * ws.element_size() if ws is not None else 0, st),
+                   px, stream, (H, last, ck, ws)), "pararnn_gated_scan_forward")
+    if sync_status:
+        _status(ws, px, stream, "pararnn_gated_scan_forward")
+    return H, last, ck
+
+
+def gated_scan_backward(px, lam, checkpoints, dL_dH, decay=8.0, reset=None, dL_dh_last=None, want_dlam=True,
+                        want_dh0=False, workspace=None, stream=None, sync_status=True):
+    """The adjoint of gated_scan_forward called with the same px, lam, decay, h0
+    and reset: returns (dL/dpx in px's dtype, dL/dlam (D) or None, dL/dh0 (B,D)
+    or None), the latter two float32.  dL_dH has px's dtype."""
+    import torch
+
+    code = _scan_shape(px, lam, 4)
+    B, T, _, D = px.shape
+    reset = _mask(reset, B, T)
+    _expect("dL_dH", dL_dH, (B, T, D), px.dtype)
+    _expect("dL_dh_last", dL_dh_last, (B, D), torch.float32)
+    _expect("checkpoints", checkpoints, (pararnn_gated_scan_checkpoint_bytes(B, T, D, code) // 4,), torch.float32)
+    _same_device(px, lam, checkpoints, dL_dH, reset, dL_dh_last, workspace)
+    dpx = torch.empty_like(px)
+    dlam = torch.empty((D,), dtype=torch.float32, device=px.device) if want_dlam else None
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=px.device) if want_dh0 else None
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(pararnn_gated_scan_workspace_bytes(B, T, D), dtype=torch.uint8, device=px.device)
+    _check(_launch(lambda st: pararnn_gated_scan_backward(B, T, D, code, px, lam, decay, reset, checkpoints, dL_dH,
+                                                          dL_dh_last, dpx, dlam, dh0, ws,
+                                                          ws.numel() * ws.element_size(), st),
+                   px, stream, (dpx, dlam, dh0, ws)), "pararnn_gated_scan_backward")
+    if sync_status:
+        _status(ws, px, stream, "pararnn_gated_scan_backward")
+    return dpx, dlam, dh0
+
+
+def gated_scan_step(px, lam, state, decay=8.0, slots=None, out=None, workspace=None, stream=None, sync_status=True):
+    """One token per row: px (N,3,D), state (n_slots,D) float32, updated in place,
+    slots (N) int32 or None (row n on slot n).  Returns y (N,D) in px's dtype; the
+    rows of padding (slot < 0) keep what `out` held (zeros if it is not given).
+    Rows that name one slot are taken in order."""
+    import torch
+
+    code = _scan_shape(px, lam, 3)
+    N, _, D = px.shape
+    if state.dim() != 2:
+        raise ValueError("state must be (n_slots, D), got %s" % (tuple(state.shape),))
+    _expect("state", state, (state.shape[0], D), torch.float32)
+    _expect("slots", slots, (N,), torch.int32)
+    _expect("out", out, (N, D), px.dtype)
+    _same_device(px, lam, state, slots, out, workspace)
+    y = out
+    if y is None:
+        make = torch.empty if slots is None else torch.zeros
+        y = make((N, D), dtype=px.dtype, device=px.device)
+    ws = _header(workspace, sync_status, px.device)
+    _check(_launch(lambda st: pararnn_gated_scan_step(N, D, code, px, lam, decay, state.shape[0], slots, state, y, ws,
+                                                      ws.numel() * ws.element_size() if ws is not None else 0, st),
+                   px, stream, (y, ws)), "pararnn_gated_scan_step")
+    if sync_status:
+        _status(ws, px, stream, "pararnn_gated_scan_step")
+    return y
+
+
+def _norm_shape(x, *params):
+    """(M, P, N) of x for scales of shape (N,) or (P..., N), which are x's last dimensions."""
+    import torch
+
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have at least one value in its last dimension, got %s" % (tuple(x.shape),))
+    shape = tuple(x.shape[-1:])
+    for t in params:
+        if t is not None:
+            shape = tuple(t.shape)
+            break
+    if not 1 <= len(shape) <= x.dim() or tuple(x.shape[x.dim() - len(shape):]) != shape or 0 in shape:
+        raise ValueError("weight and bias must have the shape of x's last dimensions, got %s for %s"
+                         % (shape, tuple(x.shape)))
+    for t in params:
+        _expect("weight and bias", t, shape, torch.float32)
+    P = 1
+    for n in shape[:-1]:
+        P *= n
+    return x.numel() // (P * shape[-1]), P, shape[-1], shape
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, workspace=None, stream=None,
+                       sync_status=True):
+    """Layer normalisation over x's last dimension, x float32 or bfloat16.
+    weight and bias (float32) are (N,), or (P, N) and so on for a scale of each
+    gate or head: the shape of x's last dimensions.  Returns (y in x's dtype,
+    mean, rstd); mean and rstd (float32, None without want_stats) are what
+    layer_norm_backward takes."""
+    import torch
+
+    code = _dtype_code(x)
+    M, P, N, _ = _norm_shape(x, weight, bias)
+    _expect("out", out, x.shape, x.dtype)
+    _same_device(x, weight, bias, out, workspace)
+    y = torch.empty_like(x) if out is None else out
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(tuple(x.shape[:-1]), dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    ws = _header(workspace, sync_status, x.device)
+    _check(_launch(lambda st: pararnn_layer_norm_forward(M, P, N, code, x, weight, bias, eps, y, mean, rstd, ws,
+                                                         ws.numel() * ws.element_size() if ws is not None else 0, st),
+                   x, stream, (y, mean, rstd, ws)), "pararnn_layer_norm_forward")
+    if sync_status:
+        _status(ws, x, stream, "pararnn_layer_norm_forward")
+    return y, mean, rstd
+
+
+def layer_norm_backward(x, dL_dy, mean, rstd, weight=None, param_shape=None, want_dparams=True, workspace=None,
+                        stream=None, sync_status=True):
+    """The gradients of layer_norm_forward: (dL/dx in x's dtype, dL/dweight,
+    dL/dbias), the latter two float32 in weight's shape (param_shape without a
+    weight, (N,) if that is not given either), or None without want_dparams."""
+    import torch
+
+    code = _dtype_code(x)
+    if weight is None and param_shape is not None:
+        weight_like = torch.empty(tuple(param_shape), dtype=torch.float32, device="meta")
+    else:
+        weight_like = weight
+    M, P, N, shape = _norm_shape(x, weight_like)
+    _expect("dL_dy", dL_dy, x.shape, x.dtype)
+    _expect("mean", mean, x.shape[:-1], torch.float32)
+    _expect("rstd", rstd, x.shape[:-1], torch.float32)
+    _same_device(x, dL_dy, mean, rstd, weight, workspace)
+    dx = torch.empty_like(x)
+    dw = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dparams else None
+    db = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dparams else None
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(pararnn_layer_norm_workspace_bytes(M, P, N), dtype=torch.uint8, device=x.device)
+    _check(_launch(lambda st: pararnn_layer_norm_backward(M, P, N, code, x, weight, mean, rstd, dL_dy, dx, dw, db, ws,
+                                                          ws.numel() * ws.element_size(), st),
+                   x, stream, (dx, dw, db, ws)), "pararnn_layer_norm_backward")
+    if sync_status:
+        _status(ws, x, stream, "pararnn_layer_norm_backward")
+    return dx, dw, db

@@ -23,6 +23,7 @@ FLAGS = [
     "-Xcompiler", "-fPIC,-O2", "-shared",
     "--expt-relaxed-constexpr",
     "-cudart", "static",
+    "--threads", "0",  # the source files compile side by side
 ]
 
 

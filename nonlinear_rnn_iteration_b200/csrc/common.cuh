@@ -13,6 +13,7 @@ namespace pararnn {
 // word 0: status bits, word 1: tile ticket counter.  The rest is padding.
 constexpr unsigned kStatusNonFinite = 1u;
 constexpr unsigned kStatusTimeout = 2u;
+constexpr unsigned kStatusBadIndex = 4u;  // an index read on the GPU was out of range
 constexpr size_t kHeaderBytes = 256;
 
 // ---- element loads -------------------------------------------------------

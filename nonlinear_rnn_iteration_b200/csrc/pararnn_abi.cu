@@ -873,6 +873,7 @@ pararnn_status pararnn_status_sync(const void* workspace, void* stream) {
     unsigned word = hdr[0];
     if (hdr[4] != 0) word = (hdr[3] == hdr[4]) ? hdr[2] : 0u;
     if (word & kStatusTimeout) return PARARNN_ETIMEOUT;
+    if (word & kStatusBadIndex) return fail(PARARNN_EINVAL, "an index in device memory is out of range");
     if (word & kStatusNonFinite) return PARARNN_ENONFINITE;
     return PARARNN_OK;
 }

@@ -9,15 +9,22 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
 #include "abi_util.cuh"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "pararnn_b200.h"
+#include "tma.cuh"
 
 namespace pararnn {
+// pararnn_abi.cu: a tensor map over (batch, steps, inner, D), box (1, rows, inner, W), zero fill outside
+pararnn_status encode_steps_map(CUtensorMap* map, const void* base, bool bf16, int64_t D, int inner, int64_t T, int64_t B,
+                                int W, int rows);
+
 namespace gs {
 
 typedef __nv_bfloat16 bf16;
@@ -38,6 +45,8 @@ struct Params {
     float* ck;             // (B, ceil(T / Ck), D) or null
     unsigned* status;      // workspace header word 0, or null
     int64_t B, T, D;
+    int64_t nCG, nCk;  // channel groups; checkpoints per batch row
+    int ranks;         // blocks per cluster
     float decay;
 };
 
@@ -93,28 +102,311 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
     return o;
 }
 
+// ---- forward ------------------------------------------------------------------
+// A block owns 64 channels of one batch row and walks T in tiles of L steps; with
+// few channels a cluster of up to 16 blocks takes that many neighbouring tiles
+// at once.  Lane l of every warp holds channels 2l, 2l+1, and warp w holds R consecutive
+// steps of the tile, so a warp's scan needs no shuffles: each thread evaluates its R steps
+// into registers (a_t, u_t), composes them into (prod a, B), and the warps' totals
+// meet in shared memory.  With a cluster each block writes its tile's element into
+// every block's shared memory, one cluster barrier per tile, and every block
+// forms the state after all of the cluster's tiles itself.  Then each
+// thread walks its R steps from the state before them and stores H.  Every
+// pre-activation is read once, by tensor copies two tiles ahead.
+constexpr int kW = 64;  // channels per block
+constexpr int kNW = 8;  // warps per block
+constexpr int kMaxRanks = 16;
+constexpr int kStages = 2;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Params pr) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= pr.B * pr.D) return;
-    const int64_t b = c / pr.D, d = c - b * pr.D;
-    const T* px = static_cast<const T*>(pr.px) + b * pr.T * 3 * pr.D + d;
-    T* H = static_cast<T*>(pr.H) + b * pr.T * pr.D + d;
-    const float k = pr.decay * softplus_f(pr.lam[d]);
-    const int64_t nck = (pr.T + Ck<T>::kSteps - 1) / Ck<T>::kSteps;
-    float h = pr.h0 ? pr.h0[c] : 0.0f;
-    bool bad = false;
-    for (int64_t t = 0; t < pr.T; ++t) {
-        if (pr.ck && t % Ck<T>::kSteps == 0) pr.ck[(b * nck + t / Ck<T>::kSteps) * pr.D + d] = h;
-        const T* p = px + t * 3 * pr.D;
-        const Row g = gates(PxTraits<T>::cvt(p[0]), PxTraits<T>::cvt(p[pr.D]), PxTraits<T>::cvt(p[2 * pr.D]), k);
-        const float u = sqrtf(g.v) * g.i * g.x;
-        h = (pr.reset && pr.reset[b * pr.T + t]) ? u : __fmaf_rn(g.a, h, u);
-        H[t * pr.D] = to_out<T>(h);
-        bad |= !isfinite(h);
+struct Tile {
+    static constexpr int R = Ck<T>::kSteps;
+    static constexpr int L = kNW * R;
+    static constexpr uint32_t kBytes = (uint32_t)(L * 3 * kW * sizeof(T));
+};
+
+// an affine map h -> P h + B of two channels
+struct Elem {
+    f2 P, B;
+};
+struct alignas(16) Totals {
+    float P[kW], B[kW];
+};
+
+template <typename T>
+struct FwdSmem {
+    alignas(128) T px[kStages][Tile<T>::L][3][kW];
+    Totals warp[2][kNW];         // each warp's element, two tiles in turn
+    Totals rank[2][kMaxRanks];   // each of the cluster's tiles, two rounds in turn
+    unsigned warp_new[2][kNW];   // whether a marked step lies in the warp's steps
+    unsigned rank_new[2][kMaxRanks];
+    uint64_t bar[kStages];
+};
+
+__device__ __forceinline__ f2 ld2(const float* p) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    return f2{v.x, v.y};
+}
+__device__ __forceinline__ f2 ld2(const bf16* p) {
+    const unsigned v = *reinterpret_cast<const unsigned*>(p);
+    return f2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+__device__ __forceinline__ void st2(float* p, f2 v) { *reinterpret_cast<float2*>(p) = make_float2(v.x, v.y); }
+__device__ __forceinline__ void st2(bf16* p, f2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+__device__ __forceinline__ void st2_cluster(float* local, uint32_t rank, f2 v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void st1_cluster(unsigned* local, uint32_t rank, unsigned v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+
+// the box of L steps and all gates of 64 channels of one batch row
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// waits for a staged tile; after one wait that ran out of time the others are short
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, bool& late) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns(), limit = late ? 1000000ull : kWaitNs;
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > limit) {
+            late = true;
+            return false;
+        }
+    return true;
+}
+
+// Two channels' decay a, and m = 1 - a, from z = y / 2 (kWide false: every y < 1):
+// m(z) = z (1 - z/2 + z^2/6 - ...) to z^8 / 8! (the next term is below 1.1e-8 of
+// it at z = 1/2), then 1 - e^-2z = m(z) (2 - m(z)).  kWide: y >= 1/2 takes the exponential as in
+// decay_of.
+template <bool kWide>
+__device__ __forceinline__ void decay2(f2 z, f2& a, f2& m) {
+    f2 s = fma2(z, splat2(-1.0f / 40320.0f), splat2(1.0f / 5040.0f));
+    s = fma2(z, s, splat2(-1.0f / 720.0f));
+    s = fma2(z, s, splat2(1.0f / 120.0f));
+    s = fma2(z, s, splat2(-1.0f / 24.0f));
+    s = fma2(z, s, splat2(1.0f / 6.0f));
+    s = fma2(z, s, splat2(-0.5f));
+    s = fma2(z, s, splat2(1.0f));
+    s = mul2(z, s);
+    m = mul2(s, sub2(splat2(2.0f), s));
+    a = sub2(splat2(1.0f), m);
+    if constexpr (kWide) {
+        const f2 e = ex2_2(mul2(z, splat2(-2.0f * kLog2e)));
+        if (z.x >= 0.25f) a.x = e.x, m.x = 1.0f - e.x;
+        if (z.y >= 0.25f) a.y = e.y, m.y = 1.0f - e.y;
     }
-    if (pr.last) pr.last[c] = h;
-    if (bad && pr.status) atomicOr(pr.status, kStatusNonFinite);
+}
+
+// a and u = sqrt(1 - a^2) sig(p_i) x.  With v = 1 - a^2 and d = 1 + e^{-p_i},
+// u = x v / sqrt(v d^2): one reciprocal square root for the root and the
+// gate's reciprocal.  d is capped at 2^62 so that d^2 stays finite, and 2^-123
+// keeps the root's argument above zero where v = 0.
+template <bool kWide>
+__device__ __forceinline__ void eval2(f2 pr, f2 pi, f2 x, f2 khalf, f2& a, f2& u) {
+    const f2 z = mul2(khalf, sigmoid2(pr));
+    f2 m;
+    decay2<kWide>(z, a, m);
+    const f2 v = mul2(m, sub2(splat2(2.0f), m));
+    const f2 d = sig_den2(pi);
+    const f2 q = fma2(mul2(v, d), d, splat2(9.4e-38f));
+    u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
+}
+
+template <typename T, bool kTma, bool kCluster>
+__global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
+    constexpr int R = Tile<T>::R, L = Tile<T>::L;
+    extern __shared__ unsigned char raw[];
+    FwdSmem<T>& sm = *reinterpret_cast<FwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
+    const int C = kCluster ? pr.ranks : 1;
+    const int64_t group = (int64_t)blockIdx.x / C;
+    const int64_t b = group / pr.nCG;
+    const int d0 = (int)(group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const bool in0 = d < pr.D, in1 = d + 1 < pr.D;
+    const int64_t row0 = b * pr.T;  // the batch row's first step in (B T)
+    const int tiles = (int)((pr.T + L - 1) / L), rounds = (tiles + C - 1) / C;
+    const T* px = static_cast<const T*>(pr.px) + row0 * 3 * pr.D;
+    T* H = static_cast<T*>(pr.H) + row0 * pr.D + d;
+
+    if (kTma && tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar[i], 1);
+        mbar_fence_init();
+    }
+    f2 khalf{0.0f, 0.0f}, carry{0.0f, 0.0f};
+    if (in0) khalf.x = 0.5f * pr.decay * softplus_f(pr.lam[d]);
+    if (in1) khalf.y = 0.5f * pr.decay * softplus_f(pr.lam[d + 1]);
+    if (pr.h0 && in0) carry.x = pr.h0[b * pr.D + d];
+    if (pr.h0 && in1) carry.y = pr.h0[b * pr.D + d + 1];
+    const bool wide = __any_sync(0xffffffffu, !(khalf.x <= 0.5f && khalf.y <= 0.5f));
+    // every block has begun, and has read h0 (h_last may be the same buffer), before a peer writes
+    if constexpr (kCluster) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    auto issue = [&](int round) {
+        const int t0 = (round * C + (int)rank) * L;
+        if (round < rounds && t0 < pr.T) {
+            uint64_t* bar = &sm.bar[round % kStages];
+            mbar_arrive_expect_tx(bar, Tile<T>::kBytes);
+            tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, (int)b);
+        }
+    };
+    if (kTma && tid == 0)
+        for (int i = 0; i < kStages; ++i) issue(i);
+    // lane j of a warp reads the mark of the warp's step j, a round ahead
+    auto marks_of = [&](int round) -> unsigned {
+        const int64_t t = (int64_t)(round * C + (int)rank) * L + warp * R + lane;
+        return (pr.reset && lane < R && round < rounds && t < pr.T) ? pr.reset[row0 + t] : 0u;
+    };
+    unsigned mark = marks_of(0);
+    bool late = false, timeout = false;
+    f2 chk{0.0f, 0.0f};  // becomes NaN once a state is not finite
+
+    for (int round = 0; round < rounds; ++round) {
+        const int par = round & 1, st = round % kStages;
+        const int tile0 = (round * C + (int)rank) * L;  // may be past T
+        const int t0 = tile0 + warp * R;
+        const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
+        mark = marks_of(round + 1);
+        f2 a[R], u[R];
+        const bool live = tile0 < pr.T;
+        if (live) {
+            if constexpr (kTma) {
+                timeout |= !wait_stage(&sm.bar[st], (round / kStages) & 1, late);
+            } else {
+                for (int i = tid; i < L * 3 * kW; i += kNW * 32) {
+                    const int row = i / (3 * kW), g = (i / kW) % 3, c = i % kW;
+                    const int64_t t = tile0 + row;
+                    sm.px[0][row][g][c] = (t < pr.T && d0 + c < pr.D) ? px[(t * 3 + g) * pr.D + d0 + c] : T(0.0f);
+                }
+                __syncthreads();
+            }
+        }
+        if (live && t0 < pr.T) {
+            const T* p = &sm.px[kTma ? st : 0][warp * R][0][2 * lane];
+            if (wide) {
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    eval2<true>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), khalf, a[j], u[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    eval2<false>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), khalf, a[j], u[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) a[j] = splat2(1.0f), u[j] = splat2(0.0f);
+        }
+        Elem e{a[0], u[0]};
+        if (marks == 0) {
+#pragma unroll
+            for (int j = 1; j < R; ++j) {
+                e.B = fma2(a[j], e.B, u[j]);
+                e.P = mul2(a[j], e.P);
+            }
+        } else {
+#pragma unroll
+            for (int j = 1; j < R; ++j) e.B = (marks >> j & 1) ? u[j] : fma2(a[j], e.B, u[j]);
+        }
+        st2(&sm.warp[par][warp].P[2 * lane], e.P);
+        st2(&sm.warp[par][warp].B[2 * lane], e.B);
+        if (lane == 0) sm.warp_new[par][warp] = marks;
+        __syncthreads();
+        if (kTma && tid == 0) issue(round + kStages);
+
+        f2 h;
+        if constexpr (kCluster) {
+            // the element of the warps before this one, and of the whole tile
+            Elem pre{splat2(1.0f), splat2(0.0f)}, all = pre;
+            unsigned pre_new = 0, all_new = 0;
+#pragma unroll
+            for (int w = 0; w < kNW; ++w) {
+                if (w == warp) pre = all, pre_new = all_new;
+                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
+                const unsigned nw = sm.warp_new[par][w];
+                all.B = nw ? B : fma2(P, all.B, B);
+                all.P = mul2(P, all.P);
+                all_new |= nw;
+            }
+            for (int r = warp; r < C; r += kNW) {
+                st2_cluster(&sm.rank[par][rank].P[2 * lane], r, all.P);
+                st2_cluster(&sm.rank[par][rank].B[2 * lane], r, all.B);
+                if (lane == 0) st1_cluster(&sm.rank_new[par][rank], r, all_new);
+            }
+            cluster_arrive_release();
+            cluster_wait_acquire();
+            f2 c = carry, mine = carry;
+            for (int r = 0; r < C; ++r) {
+                if (r == (int)rank) mine = c;
+                const f2 P = ld2(&sm.rank[par][r].P[2 * lane]), B = ld2(&sm.rank[par][r].B[2 * lane]);
+                c = sm.rank_new[par][r] ? B : fma2(P, c, B);
+            }
+            carry = c;
+            h = pre_new ? pre.B : fma2(pre.P, mine, pre.B);
+        } else {
+            f2 c = carry;
+            h = carry;
+#pragma unroll
+            for (int w = 0; w < kNW; ++w) {
+                if (w == warp) h = c;
+                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
+                c = sm.warp_new[par][w] ? B : fma2(P, c, B);
+            }
+            carry = c;
+        }
+        if (t0 >= pr.T) continue;
+        if (pr.ck) {
+            float* o = pr.ck + (b * pr.nCk + t0 / R) * pr.D + d;
+            if (in0) o[0] = h.x;
+            if (in1) o[1] = h.y;
+        }
+        T* o = H + (int64_t)t0 * pr.D;
+        const int n = (int)min((int64_t)R, pr.T - t0);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (j < n) {
+                h = (marks >> j & 1) ? u[j] : fma2(a[j], h, u[j]);
+                chk = fma2(h, splat2(0.0f), chk);
+                if constexpr (kTma) {
+                    if (in0) st2(o, h);
+                } else {
+                    if (in0) o[0] = to_out<T>(h.x);
+                    if (in1) o[1] = to_out<T>(h.y);
+                }
+            }
+            o += pr.D;
+        }
+        if (pr.last && t0 + n == pr.T) {
+            float* q = pr.last + b * pr.D + d;
+            if (in0) q[0] = h.x;
+            if (in1) q[1] = h.y;
+        }
+    }
+    if (pr.status) {
+        const bool bad = (in0 && chk.x != chk.x) || (in1 && chk.y != chk.y);
+        const unsigned bits = (__any_sync(0xffffffffu, bad) ? kStatusNonFinite : 0u) |
+                              (__any_sync(0xffffffffu, timeout) ? kStatusTimeout : 0u);
+        if (bits && lane == 0) atomicOr(pr.status, bits);
+    }
 }
 
 template <typename T>
@@ -215,12 +507,93 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams pr) {
 }
 
 bool bad_sizes(int64_t B, int64_t T, int64_t D) {
-    return B < 0 || T < 0 || D < 0 || B >= (int64_t(1) << 31) || T >= (int64_t(1) << 31) || B * T >= (int64_t(1) << 31) ||
+    return B < 0 || T < 0 || D < 0 || B >= (int64_t(1) << 31) || T > (int64_t(1) << 30) || B * T >= (int64_t(1) << 31) ||
            D >= (int64_t(1) << 31) || (double)B * T * D > 4.0e12 || (double)B * D > 1.0e11;
 }
 int64_t n_checkpoints(int64_t T, pararnn_dtype dt) {
     const int s = dt == PARARNN_F32 ? Ck<float>::kSteps : Ck<bf16>::kSteps;
     return (T + s - 1) / s;
+}
+
+// ---- launches -------------------------------------------------------------------
+// Blocks per cluster: the smallest power of two that fills the device's SMs twice
+// (two blocks are resident per SM), as far as there are tiles for them.
+int ranks_for(int64_t groups, int64_t tiles, int sms) {
+    int c = 1;
+    while (c < kMaxRanks && c < tiles && groups * c * 2 <= 2 * (int64_t)sms) c *= 2;
+    return c;
+}
+
+// A kernel's attributes are set once per device; `done` holds a bit per device.
+template <class Kern>
+bool prepare_kernel(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
+int sm_count() {
+    static thread_local int dev_of = -1, sms = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev != dev_of) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        dev_of = dev;
+    }
+    return sms;
+}
+
+template <auto kern, class P>
+pararnn_status launch_clusters(const char* who, const P& pr, const CUtensorMap& map, int64_t blocks, int ranks,
+                               size_t smem, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    if (!prepare_kernel(kern, smem, done)) return abi::cuda_fail(who, "kernel attributes not accepted");
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(kNW * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ranks;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, pr, map) == cudaSuccess ? PARARNN_OK
+                                                                  : abi::cuda_fail(who, "kernel launch failed");
+}
+
+template <typename T>
+pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
+    pr.nCG = (pr.D + kW - 1) / kW;
+    pr.nCk = n_checkpoints(pr.T, sizeof(T) == 4 ? PARARNN_F32 : PARARNN_BF16);
+    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + Tile<T>::L - 1) / Tile<T>::L;
+    pr.ranks = ranks_for(groups, tiles, sms);
+    if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
+    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16);
+    CUtensorMap map;
+    memset(&map, 0, sizeof map);
+    if (tma) {
+        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, Tile<T>::L);
+        if (s != PARARNN_OK) return s;
+    }
+    const size_t smem = sizeof(FwdSmem<T>) + 128;
+    const int64_t blocks = groups * pr.ranks;
+    if (pr.ranks > 1)
+        return tma ? launch_clusters<forward_kernel<T, true, true>>(who, pr, map, blocks, pr.ranks, smem, st)
+                   : launch_clusters<forward_kernel<T, false, true>>(who, pr, map, blocks, pr.ranks, smem, st);
+    return tma ? launch_clusters<forward_kernel<T, true, false>>(who, pr, map, blocks, 1, smem, st)
+               : launch_clusters<forward_kernel<T, false, false>>(who, pr, map, blocks, 1, smem, st);
 }
 
 }  // namespace gs
@@ -281,12 +654,7 @@ pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, parar
     pr.T = T;
     pr.D = D;
     pr.decay = decay;
-    const unsigned grid = (unsigned)((B * D + gs::kThreads - 1) / gs::kThreads);
-    if (dtype == PARARNN_F32)
-        gs::forward_kernel<float><<<grid, gs::kThreads, 0, st>>>(pr);
-    else
-        gs::forward_kernel<gs::bf16><<<grid, gs::kThreads, 0, st>>>(pr);
-    return abi::launched(who);
+    return dtype == PARARNN_F32 ? gs::launch_forward<float>(who, pr, st) : gs::launch_forward<gs::bf16>(who, pr, st);
 }
 
 pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,

@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "abi_util.cuh"
 #include "cluster.cuh"
@@ -21,9 +22,9 @@
 #include "tma.cuh"
 
 namespace pararnn {
-// pararnn_abi.cu: a tensor map over (batch, steps, inner, D), box (1, rows, inner, W), zero fill outside
+// pararnn_abi.cu: a tensor map over (B, T, inner, D), box (1, rows, gates, W), zero fill outside
 pararnn_status encode_steps_map(CUtensorMap* map, const void* base, bool bf16, int64_t D, int inner, int64_t T, int64_t B,
-                                int W, int rows);
+                                int W, int gates, int rows);
 
 namespace gs {
 
@@ -58,10 +59,12 @@ struct BwdParams {
     const void* dH;
     const float* dlast;  // (B,D) or null
     void* dpx;
-    float* part;  // (B,D)
+    float* part;  // (B * ranks, D)
     float* dh0;   // (B,D) or null
     unsigned* status;
     int64_t B, T, D;
+    int64_t nCG, nCk;
+    int ranks;
     float decay;
 };
 
@@ -409,67 +412,300 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
     }
 }
 
+// ---- adjoint --------------------------------------------------------------------
+// The forward's tiles in reversed time.  The scan runs on mu_t = a_t l_t, l_t =
+// g_t + mu_{t+1}, whose elements need p_r and g only: pass 1 forms z = y / 2
+// and the element of each thread's R steps and frees those arrays' stage.
+// With the carry, each thread walks its steps backwards for l, then
+// forwards from the checkpoint, the state before its first step, for h_{t-1} and
+// the gradients: no state is read but one in R, and the forward's
+// scan is not repeated.  p_r and g have one stage, p_i and x two, so that the
+// next tile's copies all start after pass 1; 96 KB a block, two blocks per SM.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams pr) {
-    constexpr int R = Ck<T>::kSteps;
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= pr.B * pr.D) return;
-    const int64_t b = c / pr.D, d = c - b * pr.D;
-    const T* px = static_cast<const T*>(pr.px) + b * pr.T * 3 * pr.D + d;
-    const T* dH = static_cast<const T*>(pr.dH) + b * pr.T * pr.D + d;
-    T* dpx = static_cast<T*>(pr.dpx) + b * pr.T * 3 * pr.D + d;
-    const float k = pr.decay * softplus_f(pr.lam[d]);
-    const int64_t nck = (pr.T + R - 1) / R;
-    float mu = pr.dlast ? pr.dlast[c] : 0.0f, sum = 0.0f;
-    bool bad = false;
-    for (int64_t q = nck - 1; q >= 0; --q) {
-        float before[R];
-        float h = pr.ck[(b * nck + q) * pr.D + d];
-        for (int j = 0; j < R; ++j) {
-            const int64_t t = q * R + j;
-            if (t >= pr.T) break;
-            const T* p = px + t * 3 * pr.D;
-            const Row g = gates(PxTraits<T>::cvt(p[0]), PxTraits<T>::cvt(p[pr.D]), PxTraits<T>::cvt(p[2 * pr.D]), k);
-            if (pr.reset && pr.reset[b * pr.T + t]) h = 0.0f;
-            before[j] = h;
-            h = __fmaf_rn(g.a, h, sqrtf(g.v) * g.i * g.x);
-        }
-        float part = 0.0f;
-        for (int j = R - 1; j >= 0; --j) {
-            const int64_t t = q * R + j;
-            if (t >= pr.T) continue;
-            const T* p = px + t * 3 * pr.D;
-            T* o = dpx + t * 3 * pr.D;
-            const Row g = gates(PxTraits<T>::cvt(p[0]), PxTraits<T>::cvt(p[pr.D]), PxTraits<T>::cvt(p[2 * pr.D]), k);
-            const float l = PxTraits<T>::cvt(dH[t * pr.D]) + mu;
-            const float rs = g.v > 0.0f ? rsqrtf(g.v) : 0.0f;
-            const float dx = l * (g.v * rs) * g.i;
-            const float ah = g.a * before[j];
-            const float w = g.y * l * (g.a * g.a * rs * g.i * g.x - ah);
-            const float dpr = w * (1.0f - g.r);
-            o[0] = to_out<T>(dpr);
-            o[pr.D] = to_out<T>(dx * g.x * (1.0f - g.i));
-            o[2 * pr.D] = to_out<T>(dx);
-            part += w;
-            bad |= !isfinite(dpr) || !isfinite(dx);
-            mu = (pr.reset && pr.reset[b * pr.T + t]) ? 0.0f : g.a * l;
-        }
-        sum += part;
-    }
-    if (pr.dh0) pr.dh0[c] = mu;
-    pr.part[c] = sum;
-    if (bad) atomicOr(pr.status, kStatusNonFinite);
+struct BwdSmem {
+    alignas(128) T pr[Tile<T>::L][kW];
+    alignas(128) T g[Tile<T>::L][kW];
+    alignas(128) T ix[kStages][Tile<T>::L][2][kW];
+    Totals warp[2][kNW];
+    Totals rank[2][kMaxRanks];
+    unsigned warp_new[2][kNW];
+    unsigned rank_new[2][kMaxRanks];
+    float sum[kNW][kW];
+    uint64_t bar_a, bar_b[kStages];
+};
+
+struct BwdMaps {
+    CUtensorMap pr, ix, g;  // boxes of one gate, of two gates, and of dL/dH
+};
+
+// the gradients of one step of two channels; h is h_{t-1} in and h_t out
+template <bool kWide>
+__device__ __forceinline__ void grads2(f2 z, f2 l, f2 pi, f2 x, f2 kinv, bool first, f2& h, f2& dpr, f2& dpi, f2& dx, f2& w) {
+    f2 a, m;
+    decay2<kWide>(z, a, m);
+    const f2 v = mul2(m, sub2(splat2(2.0f), m));
+    // 1 / b; the addend keeps the root's argument above zero, and where v = 0 so is z, which scales the result
+    const f2 va = add2(v, splat2(1e-37f));
+    const f2 rs{rsqrt_approx(va.x), rsqrt_approx(va.y)};
+    const f2 i = rcp_2(sig_den2(pi));
+    const f2 ib = mul2(rs, i);          // i / b
+    const f2 bi = mul2(v, ib);          // b i
+    const f2 e = mul2(ib, x);           // i x / b
+    if (first) h = splat2(0.0f);
+    const f2 ah = mul2(a, h);
+    dx = mul2(l, bi);
+    dpi = mul2(mul2(dx, x), sub2(splat2(1.0f), i));
+    w = mul2(mul2(add2(z, z), l), sub2(mul2(mul2(a, a), e), ah));
+    dpr = mul2(w, sub2(splat2(1.0f), mul2(z, kinv)));
+    h = fma2(v, e, ah);
 }
 
-// dL/dlambda = sig(lambda) / softplus(lambda) * sum over b of the partials, in order
-__global__ void dlam_kernel(const float* part, const float* lam, float* dlam, int64_t B, int64_t D) {
-    const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (d >= D) return;
+template <typename T, bool kTma, bool kCluster>
+__global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
+    constexpr int R = Tile<T>::R, L = Tile<T>::L;
+    extern __shared__ unsigned char raw[];
+    BwdSmem<T>& sm = *reinterpret_cast<BwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
+    const int C = kCluster ? pr.ranks : 1;
+    const int64_t group = (int64_t)blockIdx.x / C;
+    const int64_t b = group / pr.nCG;
+    const int d0 = (int)(group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const bool in0 = d < pr.D, in1 = d + 1 < pr.D;
+    const int64_t row0 = b * pr.T;
+    const int tiles = (int)((pr.T + L - 1) / L), rounds = (tiles + C - 1) / C;
+    const T* px = static_cast<const T*>(pr.px) + row0 * 3 * pr.D;
+    const T* dH = static_cast<const T*>(pr.dH) + row0 * pr.D;
+    T* dpx = static_cast<T*>(pr.dpx) + row0 * 3 * pr.D + d;
+
+    if (kTma && tid == 0) {
+        mbar_init(&sm.bar_a, 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar_b[i], 1);
+        mbar_fence_init();
+    }
+    f2 khalf{0.0f, 0.0f}, carry{0.0f, 0.0f};
+    if (in0) khalf.x = 0.5f * pr.decay * softplus_f(pr.lam[d]);
+    if (in1) khalf.y = 0.5f * pr.decay * softplus_f(pr.lam[d + 1]);
+    if (pr.dlast && in0) carry.x = pr.dlast[b * pr.D + d];
+    if (pr.dlast && in1) carry.y = pr.dlast[b * pr.D + d + 1];
+    // r = z / khalf; a khalf this small gives no gradient to p_r (w is below 2^-60 l)
+    const f2 kinv{khalf.x > 1e-37f ? 1.0f / khalf.x : 0.0f, khalf.y > 1e-37f ? 1.0f / khalf.y : 0.0f};
+    const bool wide = __any_sync(0xffffffffu, !(khalf.x <= 0.5f && khalf.y <= 0.5f));
+    if constexpr (kCluster) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    // round q takes the cluster's tiles from the last ones on; only round 0 may have tiles past T
+    auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
+    const int q0 = tile_of(0) < tiles ? 0 : 1;
+    auto issue = [&](int q) {
+        if (q >= rounds) return;
+        const int t0 = tile_of(q) * L, sb = (q - q0) % kStages;
+        mbar_arrive_expect_tx(&sm.bar_a, (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.pr, &maps.pr, &sm.bar_a, d0, 0, t0, (int)b);
+        tma_load_4d(sm.g, &maps.g, &sm.bar_a, d0, 0, t0, (int)b);
+        mbar_arrive_expect_tx(&sm.bar_b[sb], (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.ix[sb], &maps.ix, &sm.bar_b[sb], d0, 1, t0, (int)b);
+    };
+    if (kTma && tid == 0) issue(q0);
+    auto marks_of = [&](int q) -> unsigned {
+        if (q >= rounds) return 0u;
+        const int64_t t = (int64_t)tile_of(q) * L + warp * R + lane;
+        return (pr.reset && lane < R && t < pr.T) ? pr.reset[row0 + t] : 0u;
+    };
+    unsigned mark = marks_of(0);
+    bool late = false, timeout = false;
+    f2 chk{0.0f, 0.0f}, sum{0.0f, 0.0f};
+
+    for (int q = 0; q < rounds; ++q) {
+        const int par = q & 1, n_in = q - q0, sb = kTma ? n_in % kStages : 0;
+        const int tile0 = tile_of(q) * L, t0 = tile0 + warp * R;
+        const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
+        mark = marks_of(q + 1);
+        const bool live = q >= q0;
+        const int n = live ? (int)max((int64_t)0, min((int64_t)R, pr.T - t0)) : 0;  // this warp's steps
+        if (live) {
+            if constexpr (kTma) {
+                timeout |= !wait_stage(&sm.bar_a, n_in & 1, late);
+            } else {
+                __syncthreads();  // the tile before has been read
+                for (int i = tid; i < L * 4 * kW; i += kNW * 32) {
+                    const int row = i / (4 * kW), g = (i / kW) % 4, c = i % kW;
+                    const int64_t t = tile0 + row;
+                    T val = T(0.0f);
+                    if (t < pr.T && d0 + c < pr.D) val = g < 3 ? px[(t * 3 + g) * pr.D + d0 + c] : dH[t * pr.D + d0 + c];
+                    T* to = g == 0 ? &sm.pr[row][c] : g == 3 ? &sm.g[row][c] : &sm.ix[0][row][g - 1][c];
+                    *to = val;
+                }
+                __syncthreads();
+            }
+        }
+        // pass 1: z, g and the element of mu over the warp's steps
+        f2 z[R], l[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            z[j] = l[j] = splat2(0.0f);
+            if (j < n) {
+                z[j] = mul2(khalf, sigmoid2(ld2(&sm.pr[warp * R + j][2 * lane])));
+                l[j] = ld2(&sm.g[warp * R + j][2 * lane]);
+            }
+        }
+        Elem e{splat2(1.0f), splat2(0.0f)};
+        auto compose = [&](auto w) {
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                f2 a, m;
+                decay2<decltype(w)::value>(z[j], a, m);
+                e.B = mul2(a, add2(l[j], e.B));
+                e.P = mul2(a, e.P);
+                if (marks >> j & 1) e.B = splat2(0.0f);
+            }
+        };
+        if (wide)
+            compose(std::true_type{});
+        else
+            compose(std::false_type{});
+        st2(&sm.warp[par][warp].P[2 * lane], e.P);
+        st2(&sm.warp[par][warp].B[2 * lane], e.B);
+        if (lane == 0) sm.warp_new[par][warp] = marks;
+        __syncthreads();
+        if (kTma && live && tid == 0) issue(q + 1);
+
+        f2 mu;
+        if constexpr (kCluster) {
+            Elem pre{splat2(1.0f), splat2(0.0f)}, all = pre;
+            unsigned pre_new = 0, all_new = 0;
+#pragma unroll
+            for (int w = kNW - 1; w >= 0; --w) {
+                if (w == warp) pre = all, pre_new = all_new;
+                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
+                const unsigned nw = sm.warp_new[par][w];
+                all.B = nw ? B : fma2(P, all.B, B);
+                all.P = mul2(P, all.P);
+                all_new |= nw;
+            }
+            for (int r = warp; r < C; r += kNW) {
+                st2_cluster(&sm.rank[par][rank].P[2 * lane], r, all.P);
+                st2_cluster(&sm.rank[par][rank].B[2 * lane], r, all.B);
+                if (lane == 0) st1_cluster(&sm.rank_new[par][rank], r, all_new);
+            }
+            cluster_arrive_release();
+            cluster_wait_acquire();
+            f2 c = carry, mine = carry;
+            for (int r = C - 1; r >= 0; --r) {
+                if (r == (int)rank) mine = c;
+                const f2 P = ld2(&sm.rank[par][r].P[2 * lane]), B = ld2(&sm.rank[par][r].B[2 * lane]);
+                c = sm.rank_new[par][r] ? B : fma2(P, c, B);
+            }
+            carry = c;
+            mu = pre_new ? pre.B : fma2(pre.P, mine, pre.B);
+        } else {
+            f2 c = carry;
+            mu = carry;
+#pragma unroll
+            for (int w = kNW - 1; w >= 0; --w) {
+                if (w == warp) mu = c;
+                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
+                c = sm.warp_new[par][w] ? B : fma2(P, c, B);
+            }
+            carry = c;
+        }
+        if (kTma && live) timeout |= !wait_stage(&sm.bar_b[sb], (n_in / kStages) & 1, late);
+        if (n == 0) continue;
+        // pass 2: l backwards, then the gradients forwards from the checkpoint
+        f2 h{0.0f, 0.0f};
+        const float* ck = pr.ck + (b * pr.nCk + t0 / R) * pr.D + d;
+        if (in0) h.x = ck[0];
+        if (in1) h.y = ck[1];
+        T* o = dpx + (int64_t)t0 * 3 * pr.D;
+        f2 part{0.0f, 0.0f};
+        auto finish = [&](auto w) {
+            constexpr bool kWide = decltype(w)::value;
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                f2 a, m;
+                decay2<kWide>(z[j], a, m);
+                l[j] = add2(l[j], mu);
+                mu = mul2(a, l[j]);
+                if (marks >> j & 1) mu = splat2(0.0f);
+            }
+            const T* s = &sm.ix[sb][warp * R][0][2 * lane];
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                if (j < n) {
+                    // evaluated again from z: a and m of all R steps would not stay in registers
+                    asm volatile("" : "+f"(z[j].x), "+f"(z[j].y));
+                    f2 dpr, dpi, dx, ww;
+                    grads2<kWide>(z[j], l[j], ld2(s + j * 2 * kW), ld2(s + (j * 2 + 1) * kW), kinv, marks >> j & 1, h, dpr,
+                                  dpi, dx, ww);
+                    part = add2(part, ww);
+                    chk = fma2(dx, splat2(0.0f), chk);
+                    if constexpr (kTma) {
+                        if (in0) {
+                            st2(o, dpr);
+                            st2(o + pr.D, dpi);
+                            st2(o + 2 * pr.D, dx);
+                        }
+                    } else {
+                        if (in0) o[0] = to_out<T>(dpr.x), o[pr.D] = to_out<T>(dpi.x), o[2 * pr.D] = to_out<T>(dx.x);
+                        if (in1) o[1] = to_out<T>(dpr.y), o[pr.D + 1] = to_out<T>(dpi.y), o[2 * pr.D + 1] = to_out<T>(dx.y);
+                    }
+                }
+                o += 3 * pr.D;
+            }
+        };
+        if (wide)
+            finish(std::true_type{});
+        else
+            finish(std::false_type{});
+        sum = add2(sum, part);
+        if (t0 == 0 && pr.dh0) {
+            float* q = pr.dh0 + b * pr.D + d;
+            if (in0) q[0] = mu.x;
+            if (in1) q[1] = mu.y;
+        }
+    }
+    // the warps' sums of w in order; a sum that is not finite stands for a dL/dp_r that is not
+    st2(&sm.sum[warp][2 * lane], sum);
+    __syncthreads();
+    if (tid < kW && d0 + tid < pr.D) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) s += sm.sum[w][tid];
+        pr.part[(b * C + rank) * pr.D + d0 + tid] = s;
+    }
+    chk = fma2(sum, splat2(0.0f), chk);
+    const bool bad = (in0 && chk.x != chk.x) || (in1 && chk.y != chk.y);
+    const unsigned bits = (__any_sync(0xffffffffu, bad) ? kStatusNonFinite : 0u) |
+                          (__any_sync(0xffffffffu, timeout) ? kStatusTimeout : 0u);
+    if (bits && lane == 0) atomicOr(pr.status, bits);
+}
+
+// dL/dlambda = sig(lambda) / softplus(lambda) * the sum of the blocks' partial
+// sums: lane = channel, each warp every sixteenth row in order, then the warps in order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) dlam_kernel(const float* part, const float* lam, float* dlam, int64_t rows,
+                                                              int64_t D) {
+    __shared__ float acc[kSumWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t d = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int64_t b = 0; b < B; ++b) s += part[b * D + d];
-    const float l = lam[d];
-    const float ratio = l < -15.0f ? 1.0f : 1.0f / ((1.0f + expf(-l)) * softplus_f(l));
-    dlam[d] = ratio * s;
+    if (d < D)
+#pragma unroll 4
+        for (int64_t r = warp; r < rows; r += kSumWarps) s += part[r * D + d];
+    acc[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && d < D) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSumWarps; ++w) s += acc[w][lane];
+        const float l = lam[d];
+        // softplus(l) is sig(l) to within e^l for very negative l
+        const float ratio = l < -20.0f ? 1.0f : 1.0f / ((1.0f + expf(-l)) * softplus_f(l));
+        dlam[d] = ratio * s;
+    }
 }
 
 struct StepParams {
@@ -549,8 +785,8 @@ int sm_count() {
     return sms;
 }
 
-template <auto kern, class P>
-pararnn_status launch_clusters(const char* who, const P& pr, const CUtensorMap& map, int64_t blocks, int ranks,
+template <auto kern, class P, class Map>
+pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int64_t blocks, int ranks,
                                size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     if (!prepare_kernel(kern, smem, done)) return abi::cuda_fail(who, "kernel attributes not accepted");
@@ -572,6 +808,41 @@ pararnn_status launch_clusters(const char* who, const P& pr, const CUtensorMap& 
 }
 
 template <typename T>
+pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
+    constexpr int L = Tile<T>::L;
+    pr.nCG = (pr.D + kW - 1) / kW;
+    pr.nCk = n_checkpoints(pr.T, sizeof(T) == 4 ? PARARNN_F32 : PARARNN_BF16);
+    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
+    pr.ranks = ranks_for(groups, tiles, sms);
+    if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
+    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.dH, 16) &&
+                     !abi::misaligned(pr.dpx, 16);
+    BwdMaps maps;
+    memset(&maps, 0, sizeof maps);
+    if (tma) {
+        const bool bf = sizeof(T) == 2;
+        pararnn_status s = encode_steps_map(&maps.pr, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 1, L);
+        if (s == PARARNN_OK) s = encode_steps_map(&maps.ix, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 2, L);
+        if (s == PARARNN_OK) s = encode_steps_map(&maps.g, pr.dH, bf, pr.D, 1, pr.T, pr.B, kW, 1, L);
+        if (s != PARARNN_OK) return s;
+    }
+    const size_t smem = sizeof(BwdSmem<T>) + 128;
+    const int64_t blocks = groups * pr.ranks;
+    pararnn_status s;
+    if (pr.ranks > 1)
+        s = tma ? launch_clusters<backward_kernel<T, true, true>>(who, pr, maps, blocks, pr.ranks, smem, st)
+                : launch_clusters<backward_kernel<T, false, true>>(who, pr, maps, blocks, pr.ranks, smem, st);
+    else
+        s = tma ? launch_clusters<backward_kernel<T, true, false>>(who, pr, maps, blocks, 1, smem, st)
+                : launch_clusters<backward_kernel<T, false, false>>(who, pr, maps, blocks, 1, smem, st);
+    if (s != PARARNN_OK || !dlam) return s;
+    dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.ranks, pr.D);
+    return abi::launched(who);
+}
+
+template <typename T>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
@@ -584,7 +855,7 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     CUtensorMap map;
     memset(&map, 0, sizeof map);
     if (tma) {
-        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, Tile<T>::L);
+        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, Tile<T>::L);
         if (s != PARARNN_OK) return s;
     }
     const size_t smem = sizeof(FwdSmem<T>) + 128;
@@ -610,7 +881,8 @@ size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, para
 
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D) {
     if (gs::bad_sizes(B, T, D)) return 0;
-    return kHeaderBytes + (size_t)(B * D) * sizeof(float);
+    // a partial sum of dL/dlambda from each block of a cluster of up to 16
+    return kHeaderBytes + (size_t)(B * D) * gs::kMaxRanks * sizeof(float);
 }
 
 pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
@@ -703,15 +975,8 @@ pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, para
     pr.T = T;
     pr.D = D;
     pr.decay = decay;
-    const unsigned grid = (unsigned)((B * D + gs::kThreads - 1) / gs::kThreads);
-    if (dtype == PARARNN_F32)
-        gs::backward_kernel<float><<<grid, gs::kThreads, 0, st>>>(pr);
-    else
-        gs::backward_kernel<gs::bf16><<<grid, gs::kThreads, 0, st>>>(pr);
-    s = abi::launched(who);
-    if (s != PARARNN_OK || !dL_dlambda) return s;
-    gs::dlam_kernel<<<(unsigned)((D + 127) / 128), 128, 0, st>>>(pr.part, lambda, dL_dlambda, B, D);
-    return abi::launched(who);
+    return dtype == PARARNN_F32 ? gs::launch_backward<float>(who, pr, dL_dlambda, st)
+                                : gs::launch_backward<gs::bf16>(who, pr, dL_dlambda, st);
 }
 
 pararnn_status pararnn_gated_scan_step(int64_t N, int64_t D, pararnn_dtype dtype, const void* preacts,

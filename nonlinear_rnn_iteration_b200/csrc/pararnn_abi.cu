@@ -579,16 +579,16 @@ namespace pararnn {
 void set_last_error(const char* msg) { fail(PARARNN_OK, "%s", msg); }
 bool pointer_on_device(const void* p) { return device_reachable(p); }
 
-// 4-D map over a (B, T, inner, D) row-major tensor: box (W, inner, rows, 1),
+// 4-D map over a (B, T, inner, D) row-major tensor: box (W, gates, rows, 1),
 // zero fill outside, so that rows past T are zeros and not the next batch row's
 pararnn_status encode_steps_map(CUtensorMap* map, const void* base, bool bf16, int64_t D, int inner, int64_t T,
-                                int64_t B, int W, int rows) {
+                                int64_t B, int W, int gates, int rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(PARARNN_ECUDA, "cuTensorMapEncodeTiled is unavailable");
     const cuuint64_t row = (cuuint64_t)(D * (bf16 ? 2 : 4));
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)inner, (cuuint64_t)T, (cuuint64_t)B};
     cuuint64_t strides[3] = {row, row * inner, row * inner * (cuuint64_t)T};
-    cuuint32_t box[4] = {(cuuint32_t)W, (cuuint32_t)inner, (cuuint32_t)rows, 1};
+    cuuint32_t box[4] = {(cuuint32_t)W, (cuuint32_t)gates, (cuuint32_t)rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

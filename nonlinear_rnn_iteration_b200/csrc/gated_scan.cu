@@ -30,11 +30,8 @@ namespace gs {
 
 typedef __nv_bfloat16 bf16;
 constexpr int kThreads = 128;
-// steps between two states that the forward keeps for the adjoint
-template <typename T>
-struct Ck {
-    static constexpr int kSteps = sizeof(T) == 4 ? 8 : 16;
-};
+// steps between two states that the forward keeps for the adjoint: a warp's share of a tile
+constexpr int kCkSteps = 8;
 
 struct Params {
     const void* px;        // (B,T,3,D)
@@ -46,7 +43,7 @@ struct Params {
     float* ck;             // (B, ceil(T / Ck), D) or null
     unsigned* status;      // workspace header word 0, or null
     int64_t B, T, D;
-    int64_t nCG, nCk;  // channel groups; checkpoints per batch row
+    int nCG, nCk;  // channel groups; checkpoints per batch row
     int ranks;         // blocks per cluster
     float decay;
 };
@@ -63,7 +60,7 @@ struct BwdParams {
     float* dh0;   // (B,D) or null
     unsigned* status;
     int64_t B, T, D;
-    int64_t nCG, nCk;
+    int nCG, nCk;
     int ranks;
     float decay;
 };
@@ -106,45 +103,56 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 }
 
 // ---- forward ------------------------------------------------------------------
-// A block owns 64 channels of one batch row and walks T in tiles of L steps; with
-// few channels a cluster of up to 16 blocks takes that many neighbouring tiles
-// at once.  Lane l of every warp holds channels 2l, 2l+1, and warp w holds R consecutive
-// steps of the tile, so a warp's scan needs no shuffles: each thread evaluates its R steps
-// into registers (a_t, u_t), composes them into (prod a, B), and the warps' totals
-// meet in shared memory.  With a cluster each block writes its tile's element into
-// every block's shared memory, one cluster barrier per tile, and every block
-// forms the state after all of the cluster's tiles itself.  Then each
-// thread walks its R steps from the state before them and stores H.  Every
-// pre-activation is read once, by tensor copies two tiles ahead.
+// A block owns 64 channels of one batch row and walks T in tiles of 8 R steps; with
+// few channels a cluster of up to 8 blocks takes that many neighbouring tiles
+// at once (a round).  Lane l of every warp holds channels 2l, 2l+1, and warp w holds R
+// consecutive steps of the tile, so a warp's scan needs no shuffles: each thread evaluates
+// its R steps into registers (a_t, u_t), composes them into h -> P h + B, and after one block
+// barrier per tile applies the elements of the warps before it to the carry and walks its
+// steps.  The last warp forms the carry of the next tile.  In a cluster the last warp
+// first sends the tile's element into every block's shared memory, where an
+// mbarrier counts the bytes: no block waits for more than the data it needs.
+// Every pre-activation is read once, by tensor copies two or more tiles ahead.
 constexpr int kW = 64;  // channels per block
 constexpr int kNW = 8;  // warps per block
-constexpr int kMaxRanks = 16;
-constexpr int kStages = 2;
+constexpr int kMaxRanks = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <typename T>
 struct Tile {
-    static constexpr int R = Ck<T>::kSteps;
-    static constexpr int L = kNW * R;
-    static constexpr uint32_t kBytes = (uint32_t)(L * 3 * kW * sizeof(T));
+    static constexpr int R = kCkSteps, L = kNW * R;
 };
 
-// an affine map h -> P h + B of two channels
+// An affine map h -> P h + B of two channels.  P is a product of decays, 0 to
+// 1; P = -1 stands for a map through a marked step, which is h -> B for every h.
 struct Elem {
     f2 P, B;
 };
-struct alignas(16) Totals {
-    float P[kW], B[kW];
-};
+__device__ __forceinline__ float4 pack(const Elem& e) { return make_float4(e.P.x, e.P.y, e.B.x, e.B.y); }
+__device__ __forceinline__ Elem unpack(float4 v) { return Elem{f2{v.x, v.y}, f2{v.z, v.w}}; }
+template <bool kCuts>
+__device__ __forceinline__ f2 apply(const Elem& e, f2 h) {
+    const f2 to = fma2(e.P, h, e.B);
+    if (kCuts && e.P.x < 0.0f) return e.B;
+    return to;
+}
+// first `e`, then `f`
+template <bool kCuts>
+__device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
+    Elem o{mul2(f.P, e.P), fma2(f.P, e.B, f.B)};
+    if (kCuts && f.P.x < 0.0f) o = f;
+    if (kCuts && e.P.x < 0.0f) o.P = splat2(-1.0f);
+    return o;
+}
 
 template <typename T>
 struct FwdSmem {
+    static constexpr int kStages = 8 / sizeof(T);
     alignas(128) T px[kStages][Tile<T>::L][3][kW];
-    Totals warp[2][kNW];         // each warp's element, two tiles in turn
-    Totals rank[2][kMaxRanks];   // each of the cluster's tiles, two rounds in turn
-    unsigned warp_new[2][kNW];   // whether a marked step lies in the warp's steps
-    unsigned rank_new[2][kMaxRanks];
-    uint64_t bar[kStages];
+    float4 warp[2][kNW][32];        // each warp's element, two rounds in turn
+    float4 rank[2][kMaxRanks][32];  // each of the cluster's tiles
+    float2 carry[2][32];            // the state before the round
+    uint64_t bar[kStages], rank_bar[2];
 };
 
 __device__ __forceinline__ f2 ld2(const float* p) {
@@ -160,18 +168,17 @@ __device__ __forceinline__ void st2(bf16* p, f2 v) {
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 
-__device__ __forceinline__ void st2_cluster(float* local, uint32_t rank, f2 v) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
-}
-__device__ __forceinline__ void st1_cluster(unsigned* local, uint32_t rank, unsigned v) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+// 16 bytes to the same place of block `rank` of the cluster, counted on its mbarrier
+__device__ __forceinline__ void send16(float4* local, uint64_t* local_bar, uint32_t rank, float4 v) {
+    uint32_t to, bar;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(local_bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to),
+                 "r"(bar), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 
-// the box of L steps and all gates of 64 channels of one batch row
+// the box of a tile's steps, of some gates and 64 channels of one batch row
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
     asm volatile(
@@ -181,84 +188,102 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
-// waits for a staged tile; after one wait that ran out of time the others are short
-__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, bool& late) {
-    if (mbar_try_wait(bar, parity)) return true;
+// a wait with a limit; after one that ran out of time the others are short
+template <bool kPeers>
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& late) {
+    if (kPeers ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return;
     const uint64_t t0 = globaltimer_ns(), limit = late ? 1000000ull : kWaitNs;
-    while (!mbar_try_wait(bar, parity))
+    while (!(kPeers ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
         if (globaltimer_ns() - t0 > limit) {
             late = true;
-            return false;
+            return;
         }
-    return true;
 }
 
-// Two channels' decay a, and m = 1 - a, from z = y / 2 (kWide false: every y < 1):
-// m(z) = z (1 - z/2 + z^2/6 - ...) to z^8 / 8! (the next term is below 1.1e-8 of
-// it at z = 1/2), then 1 - e^-2z = m(z) (2 - m(z)).  kWide: y >= 1/2 takes the exponential as in
-// decay_of.
+// Two channels' decay a = e^-y and m = 1 - a.  For y <= 1 m is y times the polynomial
+// of degree 6 through (1 - e^-y) / y at the seven Chebyshev points of [0, 1], off by
+// at most 2.4e-8 of it with its coefficients in float32, and a is 1 - m, rounded
+// to nearest: an error of a that leans to one side would add up over a memory of 1/m
+// steps.  kWide, for decays that reach past 1: there a is the exponential, which keeps the
+// digits of a small a.
 template <bool kWide>
-__device__ __forceinline__ void decay2(f2 z, f2& a, f2& m) {
-    f2 s = fma2(z, splat2(-1.0f / 40320.0f), splat2(1.0f / 5040.0f));
-    s = fma2(z, s, splat2(-1.0f / 720.0f));
-    s = fma2(z, s, splat2(1.0f / 120.0f));
-    s = fma2(z, s, splat2(-1.0f / 24.0f));
-    s = fma2(z, s, splat2(1.0f / 6.0f));
-    s = fma2(z, s, splat2(-0.5f));
-    s = fma2(z, s, splat2(1.0f));
-    s = mul2(z, s);
-    m = mul2(s, sub2(splat2(2.0f), s));
+__device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
+    f2 s = fma2(y, splat2(1.29076303e-4f), splat2(-1.30077498e-3f));
+    s = fma2(y, s, splat2(8.27550516e-3f));
+    s = fma2(y, s, splat2(-4.16468494e-2f));
+    s = fma2(y, s, splat2(1.66663408e-1f));
+    s = fma2(y, s, splat2(-4.99999791e-1f));
+    s = fma2(y, s, splat2(1.0f));
+    m = mul2(y, s);
     a = sub2(splat2(1.0f), m);
     if constexpr (kWide) {
-        const f2 e = ex2_2(mul2(z, splat2(-2.0f * kLog2e)));
-        if (z.x >= 0.25f) a.x = e.x, m.x = 1.0f - e.x;
-        if (z.y >= 0.25f) a.y = e.y, m.y = 1.0f - e.y;
+        const f2 e = ex2_2(mul2(y, splat2(-kLog2e)));
+        if (y.x > 1.0f) a.x = e.x, m.x = 1.0f - e.x;
+        if (y.y > 1.0f) a.y = e.y, m.y = 1.0f - e.y;
+        // a NaN decay takes the polynomial, which keeps it
     }
 }
+__device__ __forceinline__ f2 exp_neg2(f2 x) { return ex2_2(mul2(x, splat2(-kLog2e))); }
 
-// a and u = sqrt(1 - a^2) sig(p_i) x.  With v = 1 - a^2 and d = 1 + e^{-p_i},
-// u = x v / sqrt(v d^2): one reciprocal square root for the root and the
-// gate's reciprocal.  d is capped at 2^62 so that d^2 stays finite, and 2^-123
-// keeps the root's argument above zero where v = 0.
+// sig of two channels with one reciprocal (simultaneous inversion, as in inv_pair):
+// the special-function unit, 16 lanes a cycle and SM, is what the evaluation is
+// bound by.  Where the product of the denominators nears the float range each has its own.
+__device__ __forceinline__ f2 sigmoid_pair(f2 x) {
+    const f2 d = add2(exp_neg2(x), splat2(1.0f));
+    const float p = d.x * d.y, q = rcp_approx(p);
+    f2 r{d.y * q, d.x * q};
+    if (!(p <= 1e37f)) r = rcp_2(d);
+    return r;
+}
+
+// a and u = sqrt(1 - a^2) sig(p_i) x.  With v = 1 - a^2 = m (1 + a) and d = 1 + e^{-p_i},
+// u = x v / sqrt(v d^2): one reciprocal square root for the root and the gate's reciprocal.
+// An infinite d gives u = 0; the addend keeps v d^2 above zero where v = 0.
 template <bool kWide>
-__device__ __forceinline__ void eval2(f2 pr, f2 pi, f2 x, f2 khalf, f2& a, f2& u) {
-    const f2 z = mul2(khalf, sigmoid2(pr));
+__device__ __forceinline__ void eval2(f2 pr, f2 pi, f2 x, f2 k, f2& a, f2& u) {
+    const f2 y = mul2(k, sigmoid_pair(pr));
     f2 m;
-    decay2<kWide>(z, a, m);
-    const f2 v = mul2(m, sub2(splat2(2.0f), m));
-    const f2 d = sig_den2(pi);
-    const f2 q = fma2(mul2(v, d), d, splat2(9.4e-38f));
+    decay2<kWide>(y, a, m);
+    const f2 v = fma2(m, a, m);
+    const f2 d = add2(exp_neg2(pi), splat2(1.0f));
+    const f2 q = mul2(mul2(add2(v, splat2(1e-37f)), d), d);
     u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
 }
 
-template <typename T, bool kTma, bool kCluster>
+template <typename T, bool kTma, bool kCluster, bool kCuts>
 __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
-    constexpr int R = Tile<T>::R, L = Tile<T>::L;
+    constexpr int kStages = FwdSmem<T>::kStages, R = Tile<T>::R, L = Tile<T>::L;
     extern __shared__ unsigned char raw[];
     FwdSmem<T>& sm = *reinterpret_cast<FwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // one value for the warp
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
     const int C = kCluster ? pr.ranks : 1;
-    const int64_t group = (int64_t)blockIdx.x / C;
-    const int64_t b = group / pr.nCG;
-    const int d0 = (int)(group - b * pr.nCG) * kW, d = d0 + 2 * lane;
-    const bool in0 = d < pr.D, in1 = d + 1 < pr.D;
-    const int64_t row0 = b * pr.T;  // the batch row's first step in (B T)
-    const int tiles = (int)((pr.T + L - 1) / L), rounds = (tiles + C - 1) / C;
-    const T* px = static_cast<const T*>(pr.px) + row0 * 3 * pr.D;
-    T* H = static_cast<T*>(pr.H) + row0 * pr.D + d;
+    const int group = (int)(blockIdx.x / C), b = group / pr.nCG;
+    const int d0 = (group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const int T_ = (int)pr.T, D = (int)pr.D;
+    const bool in0 = d < D, in1 = d + 1 < D;
+    const int rounds = ((T_ + L - 1) / L + C - 1) / C;
+    const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
 
-    if (kTma && tid == 0) {
+    if (tid == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+        if (kCluster)
+            for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
-    f2 khalf{0.0f, 0.0f}, carry{0.0f, 0.0f};
-    if (in0) khalf.x = 0.5f * pr.decay * softplus_f(pr.lam[d]);
-    if (in1) khalf.y = 0.5f * pr.decay * softplus_f(pr.lam[d + 1]);
-    if (pr.h0 && in0) carry.x = pr.h0[b * pr.D + d];
-    if (pr.h0 && in1) carry.y = pr.h0[b * pr.D + d + 1];
-    const bool wide = __any_sync(0xffffffffu, !(khalf.x <= 0.5f && khalf.y <= 0.5f));
-    // every block has begun, and has read h0 (h_last may be the same buffer), before a peer writes
+    f2 k{0.0f, 0.0f};
+    if (in0) k.x = pr.decay * softplus_f(pr.lam[d]);
+    if (in1) k.y = pr.decay * softplus_f(pr.lam[d + 1]);
+    const bool wide = __any_sync(0xffffffffu, !(k.x <= 1.0f && k.y <= 1.0f));
+    if (warp == 0) {
+        f2 h{0.0f, 0.0f};
+        if (pr.h0 && in0) h.x = pr.h0[(int64_t)b * D + d];
+        if (pr.h0 && in1) h.y = pr.h0[(int64_t)b * D + d + 1];
+        sm.carry[0][lane] = make_float2(h.x, h.y);
+    }
+    // every block has begun, and has read h0 (h_last may be the same buffer)
     if constexpr (kCluster) {
         cluster_arrive_release();
         cluster_wait_acquire();
@@ -267,171 +292,169 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
     }
     auto issue = [&](int round) {
         const int t0 = (round * C + (int)rank) * L;
-        if (round < rounds && t0 < pr.T) {
+        if (round < rounds && t0 < T_) {
             uint64_t* bar = &sm.bar[round % kStages];
-            mbar_arrive_expect_tx(bar, Tile<T>::kBytes);
-            tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, (int)b);
+            mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
+            tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, b);
         }
     };
     if (kTma && tid == 0)
         for (int i = 0; i < kStages; ++i) issue(i);
     // lane j of a warp reads the mark of the warp's step j, a round ahead
     auto marks_of = [&](int round) -> unsigned {
-        const int64_t t = (int64_t)(round * C + (int)rank) * L + warp * R + lane;
-        return (pr.reset && lane < R && round < rounds && t < pr.T) ? pr.reset[row0 + t] : 0u;
+        const int t = (round * C + (int)rank) * L + warp * R + lane;
+        return (lane < R && round < rounds && t < T_) ? pr.reset[(int64_t)b * T_ + t] : 0u;
     };
-    unsigned mark = marks_of(0);
-    bool late = false, timeout = false;
-    f2 chk{0.0f, 0.0f};  // becomes NaN once a state is not finite
+    unsigned mark = kCuts ? marks_of(0) : 0u;
+    bool late = false, bad = false;
+    int t0 = (int)rank * L + warp * R;  // the warp's first step
+    T* H = static_cast<T*>(pr.H) + ((int64_t)b * T_ + t0) * D;
 
     for (int round = 0; round < rounds; ++round) {
-        const int par = round & 1, st = round % kStages;
-        const int tile0 = (round * C + (int)rank) * L;  // may be past T
-        const int t0 = tile0 + warp * R;
-        const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
-        mark = marks_of(round + 1);
-        f2 a[R], u[R];
-        const bool live = tile0 < pr.T;
-        if (live) {
+        const int par = round & 1, st = kTma ? round % kStages : 0, tile0 = t0 - warp * R;
+        unsigned marks = 0;
+        if constexpr (kCuts) {
+            marks = __ballot_sync(0xffffffffu, mark != 0);
+            mark = marks_of(round + 1);
+        }
+        if (tile0 < T_) {
             if constexpr (kTma) {
-                timeout |= !wait_stage(&sm.bar[st], (round / kStages) & 1, late);
+                wait_bar<false>(&sm.bar[st], (round / kStages) & 1, late);
             } else {
                 for (int i = tid; i < L * 3 * kW; i += kNW * 32) {
-                    const int row = i / (3 * kW), g = (i / kW) % 3, c = i % kW;
-                    const int64_t t = tile0 + row;
-                    sm.px[0][row][g][c] = (t < pr.T && d0 + c < pr.D) ? px[(t * 3 + g) * pr.D + d0 + c] : T(0.0f);
+                    const int row = i / (3 * kW), g = (i / kW) % 3, c = i % kW, t = tile0 + row;
+                    sm.px[0][row][g][c] = (t < T_ && d0 + c < D) ? px[((int64_t)t * 3 + g) * D + d0 + c] : T(0.0f);
                 }
                 __syncthreads();
             }
         }
-        if (live && t0 < pr.T) {
-            const T* p = &sm.px[kTma ? st : 0][warp * R][0][2 * lane];
+        f2 a[R], u[R];
+        Elem e{splat2(1.0f), splat2(0.0f)};
+        if (t0 < T_) {
+            const T* p = &sm.px[st][warp * R][0][2 * lane];
             if (wide) {
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    eval2<true>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), khalf, a[j], u[j]);
+                    eval2<true>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), k, a[j], u[j]);
             } else {
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    eval2<false>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), khalf, a[j], u[j]);
+                    eval2<false>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), k, a[j], u[j]);
             }
-        } else {
+            e = Elem{a[0], u[0]};
+            if (!kCuts || marks == 0) {
 #pragma unroll
-            for (int j = 0; j < R; ++j) a[j] = splat2(1.0f), u[j] = splat2(0.0f);
-        }
-        Elem e{a[0], u[0]};
-        if (marks == 0) {
+                for (int j = 1; j < R; ++j) {
+                    e.B = fma2(a[j], e.B, u[j]);
+                    e.P = mul2(a[j], e.P);
+                }
+            } else {
 #pragma unroll
-            for (int j = 1; j < R; ++j) {
-                e.B = fma2(a[j], e.B, u[j]);
-                e.P = mul2(a[j], e.P);
+                for (int j = 1; j < R; ++j) e.B = (marks >> j & 1) ? u[j] : fma2(a[j], e.B, u[j]);
+                e.P = splat2(-1.0f);
             }
-        } else {
-#pragma unroll
-            for (int j = 1; j < R; ++j) e.B = (marks >> j & 1) ? u[j] : fma2(a[j], e.B, u[j]);
         }
-        st2(&sm.warp[par][warp].P[2 * lane], e.P);
-        st2(&sm.warp[par][warp].B[2 * lane], e.B);
-        if (lane == 0) sm.warp_new[par][warp] = marks;
+        sm.warp[par][warp][lane] = pack(e);
         __syncthreads();
-        if (kTma && tid == 0) issue(round + kStages);
+        if (kTma && tid == 0) issue(round + kStages);  // every warp has read this round's stage
 
         f2 h;
         if constexpr (kCluster) {
-            // the element of the warps before this one, and of the whole tile
-            Elem pre{splat2(1.0f), splat2(0.0f)}, all = pre;
-            unsigned pre_new = 0, all_new = 0;
-#pragma unroll
-            for (int w = 0; w < kNW; ++w) {
-                if (w == warp) pre = all, pre_new = all_new;
-                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
-                const unsigned nw = sm.warp_new[par][w];
-                all.B = nw ? B : fma2(P, all.B, B);
-                all.P = mul2(P, all.P);
-                all_new |= nw;
+            Elem pre{splat2(1.0f), splat2(0.0f)};
+            for (int w = 0; w < warp; ++w) pre = then<kCuts>(pre, unpack(sm.warp[par][w][lane]));
+            if (warp == kNW - 1) {
+                const float4 all = pack(then<kCuts>(pre, e));
+                for (int r = 0; r < C; ++r) send16(&sm.rank[par][rank][lane], &sm.rank_bar[par], r, all);
             }
-            for (int r = warp; r < C; r += kNW) {
-                st2_cluster(&sm.rank[par][rank].P[2 * lane], r, all.P);
-                st2_cluster(&sm.rank[par][rank].B[2 * lane], r, all.B);
-                if (lane == 0) st1_cluster(&sm.rank_new[par][rank], r, all_new);
+            wait_bar<true>(&sm.rank_bar[par], (round >> 1) & 1, late);
+            if (tid == 0) mbar_arrive_expect_tx(&sm.rank_bar[par], C * (uint32_t)sizeof sm.rank[0][0]);
+            h = ld2(&sm.carry[par][lane].x);
+            for (int r = 0; r < (int)rank; ++r) h = apply<kCuts>(unpack(sm.rank[par][r][lane]), h);
+            if (warp == kNW - 1) {
+                f2 c = h;
+                for (int r = (int)rank; r < C; ++r) c = apply<kCuts>(unpack(sm.rank[par][r][lane]), c);
+                sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
-            cluster_arrive_release();
-            cluster_wait_acquire();
-            f2 c = carry, mine = carry;
-            for (int r = 0; r < C; ++r) {
-                if (r == (int)rank) mine = c;
-                const f2 P = ld2(&sm.rank[par][r].P[2 * lane]), B = ld2(&sm.rank[par][r].B[2 * lane]);
-                c = sm.rank_new[par][r] ? B : fma2(P, c, B);
-            }
-            carry = c;
-            h = pre_new ? pre.B : fma2(pre.P, mine, pre.B);
+            h = apply<kCuts>(pre, h);
         } else {
-            f2 c = carry;
-            h = carry;
-#pragma unroll
-            for (int w = 0; w < kNW; ++w) {
-                if (w == warp) h = c;
-                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
-                c = sm.warp_new[par][w] ? B : fma2(P, c, B);
+            h = ld2(&sm.carry[par][lane].x);
+            for (int w = 0; w < warp; ++w) h = apply<kCuts>(unpack(sm.warp[par][w][lane]), h);
+            if (warp == kNW - 1) {
+                const f2 c = apply<kCuts>(e, h);
+                sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
-            carry = c;
         }
-        if (t0 >= pr.T) continue;
-        if (pr.ck) {
-            float* o = pr.ck + (b * pr.nCk + t0 / R) * pr.D + d;
-            if (in0) o[0] = h.x;
-            if (in1) o[1] = h.y;
-        }
-        T* o = H + (int64_t)t0 * pr.D;
-        const int n = (int)min((int64_t)R, pr.T - t0);
+        if (t0 < T_) {
+            if (pr.ck) {
+                float* o = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
+                if (in0) o[0] = h.x;
+                if (in1) o[1] = h.y;
+            }
+            const int n = min(R, T_ - t0);
+            T* o = H + d;
+            if (kTma && (!kCuts || marks == 0) && n == R) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (j < n) {
-                h = (marks >> j & 1) ? u[j] : fma2(a[j], h, u[j]);
-                chk = fma2(h, splat2(0.0f), chk);
-                if constexpr (kTma) {
+                for (int j = 0; j < R; ++j) {
+                    h = fma2(a[j], h, u[j]);
                     if (in0) st2(o, h);
-                } else {
-                    if (in0) o[0] = to_out<T>(h.x);
-                    if (in1) o[1] = to_out<T>(h.y);
+                    o += D;
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (j < n) {
+                        if (kCuts && (marks >> j & 1)) {
+                            bad |= (in0 && !isfinite(h.x)) || (in1 && !isfinite(h.y));
+                            h = u[j];
+                        } else {
+                            h = fma2(a[j], h, u[j]);
+                        }
+                        if (kTma && in0) st2(o, h);
+                        if (!kTma && in0) o[0] = to_out<T>(h.x);
+                        if (!kTma && in1) o[1] = to_out<T>(h.y);
+                        o += D;
+                    }
             }
-            o += pr.D;
+            // without a marked step a state that is not finite stays so
+            bad |= (in0 && !isfinite(h.x)) || (in1 && !isfinite(h.y));
+            if (pr.last && t0 + n == T_) {
+                float* q = pr.last + (int64_t)b * D + d;
+                if (in0) q[0] = h.x;
+                if (in1) q[1] = h.y;
+            }
         }
-        if (pr.last && t0 + n == pr.T) {
-            float* q = pr.last + b * pr.D + d;
-            if (in0) q[0] = h.x;
-            if (in1) q[1] = h.y;
-        }
+        t0 += C * L;
+        H += (int64_t)C * L * D;
     }
     if (pr.status) {
-        const bool bad = (in0 && chk.x != chk.x) || (in1 && chk.y != chk.y);
         const unsigned bits = (__any_sync(0xffffffffu, bad) ? kStatusNonFinite : 0u) |
-                              (__any_sync(0xffffffffu, timeout) ? kStatusTimeout : 0u);
+                              (__any_sync(0xffffffffu, late) ? kStatusTimeout : 0u);
         if (bits && lane == 0) atomicOr(pr.status, bits);
+    }
+    // no block leaves while a peer's element may be on its way to it
+    if constexpr (kCluster) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
     }
 }
 
 // ---- adjoint --------------------------------------------------------------------
 // The forward's tiles in reversed time.  The scan runs on mu_t = a_t l_t, l_t =
-// g_t + mu_{t+1}, whose elements need p_r and g only: pass 1 forms z = y / 2
-// and the element of each thread's R steps and frees those arrays' stage.
-// With the carry, each thread walks its steps backwards for l, then
-// forwards from the checkpoint, the state before its first step, for h_{t-1} and
-// the gradients: no state is read but one in R, and the forward's
-// scan is not repeated.  p_r and g have one stage, p_i and x two, so that the
-// next tile's copies all start after pass 1; 96 KB a block, two blocks per SM.
+// g_t + mu_{t+1}, whose elements need p_r and g only: a round first forms y and
+// the elements and frees those arrays' stage.  With the carry, each thread walks its
+// steps backwards for l, then forwards from the checkpoint, the state before its
+// first step, for h_{t-1} and the gradients: of the states one in R is read, and the
+// forward's scan is not repeated.
 template <typename T>
 struct BwdSmem {
-    alignas(128) T pr[Tile<T>::L][kW];
-    alignas(128) T g[Tile<T>::L][kW];
-    alignas(128) T ix[kStages][Tile<T>::L][2][kW];
-    Totals warp[2][kNW];
-    Totals rank[2][kMaxRanks];
-    unsigned warp_new[2][kNW];
-    unsigned rank_new[2][kMaxRanks];
-    float sum[kNW][kW];
-    uint64_t bar_a, bar_b[kStages];
+    static constexpr int kA = 4 / sizeof(T), kB = kA + 1;  // stages of p_r and g, of p_i and x
+    alignas(128) T pr[kA][Tile<T>::L][kW];
+    alignas(128) T g[kA][Tile<T>::L][kW];
+    alignas(128) T ix[kB][Tile<T>::L][2][kW];
+    float4 warp[2][kNW][32];
+    float4 rank[2][kMaxRanks][32];
+    float2 carry[2][32];
+    uint64_t bar_a[kA], bar_b[kB], rank_bar[2];
 };
 
 struct BwdMaps {
@@ -440,57 +463,60 @@ struct BwdMaps {
 
 // the gradients of one step of two channels; h is h_{t-1} in and h_t out
 template <bool kWide>
-__device__ __forceinline__ void grads2(f2 z, f2 l, f2 pi, f2 x, f2 kinv, bool first, f2& h, f2& dpr, f2& dpi, f2& dx, f2& w) {
+__device__ __forceinline__ void grads2(f2 y, f2 l, f2 pi, f2 x, f2 kinv, f2& h, f2& dpr, f2& dpi, f2& dx, f2& w) {
     f2 a, m;
-    decay2<kWide>(z, a, m);
-    const f2 v = mul2(m, sub2(splat2(2.0f), m));
-    // 1 / b; the addend keeps the root's argument above zero, and where v = 0 so is z, which scales the result
+    decay2<kWide>(y, a, m);
+    const f2 v = fma2(m, a, m);
+    // 1 / b; the addend keeps the root's argument above zero, and where v = 0 so is y, which scales the result
     const f2 va = add2(v, splat2(1e-37f));
-    const f2 rs{rsqrt_approx(va.x), rsqrt_approx(va.y)};
-    const f2 i = rcp_2(sig_den2(pi));
-    const f2 ib = mul2(rs, i);          // i / b
-    const f2 bi = mul2(v, ib);          // b i
-    const f2 e = mul2(ib, x);           // i x / b
-    if (first) h = splat2(0.0f);
+    const f2 i = sigmoid_pair(pi);
+    const f2 ib = mul2(f2{rsqrt_approx(va.x), rsqrt_approx(va.y)}, i);  // i / b
+    const f2 e = mul2(ib, x);
     const f2 ah = mul2(a, h);
-    dx = mul2(l, bi);
+    dx = mul2(l, mul2(v, ib));
     dpi = mul2(mul2(dx, x), sub2(splat2(1.0f), i));
-    w = mul2(mul2(add2(z, z), l), sub2(mul2(mul2(a, a), e), ah));
-    dpr = mul2(w, sub2(splat2(1.0f), mul2(z, kinv)));
+    w = mul2(mul2(y, l), sub2(mul2(mul2(a, a), e), ah));
+    dpr = mul2(w, sub2(splat2(1.0f), mul2(y, kinv)));
     h = fma2(v, e, ah);
 }
 
-template <typename T, bool kTma, bool kCluster>
+template <typename T, bool kTma, bool kCluster, bool kCuts>
 __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
-    constexpr int R = Tile<T>::R, L = Tile<T>::L;
+    constexpr int kA = BwdSmem<T>::kA, kB = BwdSmem<T>::kB, R = Tile<T>::R, L = Tile<T>::L;
     extern __shared__ unsigned char raw[];
     BwdSmem<T>& sm = *reinterpret_cast<BwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
     const int C = kCluster ? pr.ranks : 1;
-    const int64_t group = (int64_t)blockIdx.x / C;
-    const int64_t b = group / pr.nCG;
-    const int d0 = (int)(group - b * pr.nCG) * kW, d = d0 + 2 * lane;
-    const bool in0 = d < pr.D, in1 = d + 1 < pr.D;
-    const int64_t row0 = b * pr.T;
-    const int tiles = (int)((pr.T + L - 1) / L), rounds = (tiles + C - 1) / C;
-    const T* px = static_cast<const T*>(pr.px) + row0 * 3 * pr.D;
-    const T* dH = static_cast<const T*>(pr.dH) + row0 * pr.D;
-    T* dpx = static_cast<T*>(pr.dpx) + row0 * 3 * pr.D + d;
+    const int group = (int)(blockIdx.x / C), b = group / pr.nCG;
+    const int d0 = (group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const int T_ = (int)pr.T, D = (int)pr.D;
+    const bool in0 = d < D, in1 = d + 1 < D;
+    const int tiles = (T_ + L - 1) / L, rounds = (tiles + C - 1) / C;
+    const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
+    const T* dH = static_cast<const T*>(pr.dH) + (int64_t)b * T_ * D;
 
-    if (kTma && tid == 0) {
-        mbar_init(&sm.bar_a, 1);
-        for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar_b[i], 1);
+    if (tid == 0) {
+        for (int i = 0; i < kA; ++i) mbar_init(&sm.bar_a[i], 1);
+        for (int i = 0; i < kB; ++i) mbar_init(&sm.bar_b[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+        if (kCluster)
+            for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
-    f2 khalf{0.0f, 0.0f}, carry{0.0f, 0.0f};
-    if (in0) khalf.x = 0.5f * pr.decay * softplus_f(pr.lam[d]);
-    if (in1) khalf.y = 0.5f * pr.decay * softplus_f(pr.lam[d + 1]);
-    if (pr.dlast && in0) carry.x = pr.dlast[b * pr.D + d];
-    if (pr.dlast && in1) carry.y = pr.dlast[b * pr.D + d + 1];
-    // r = z / khalf; a khalf this small gives no gradient to p_r (w is below 2^-60 l)
-    const f2 kinv{khalf.x > 1e-37f ? 1.0f / khalf.x : 0.0f, khalf.y > 1e-37f ? 1.0f / khalf.y : 0.0f};
-    const bool wide = __any_sync(0xffffffffu, !(khalf.x <= 0.5f && khalf.y <= 0.5f));
+    f2 k{0.0f, 0.0f};
+    if (in0) k.x = pr.decay * softplus_f(pr.lam[d]);
+    if (in1) k.y = pr.decay * softplus_f(pr.lam[d + 1]);
+    // r = y / k; a k this small gives no gradient to p_r (w is below 2^-60 l)
+    const f2 kinv{k.x > 1e-37f ? 1.0f / k.x : 0.0f, k.y > 1e-37f ? 1.0f / k.y : 0.0f};
+    const bool wide = __any_sync(0xffffffffu, !(k.x <= 1.0f && k.y <= 1.0f));
+    if (warp == 0) {
+        f2 mu{0.0f, 0.0f};
+        if (pr.dlast && in0) mu.x = pr.dlast[(int64_t)b * D + d];
+        if (pr.dlast && in1) mu.y = pr.dlast[(int64_t)b * D + d + 1];
+        sm.carry[0][lane] = make_float2(mu.x, mu.y);
+    }
     if constexpr (kCluster) {
         cluster_arrive_release();
         cluster_wait_acquire();
@@ -499,188 +525,206 @@ __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams p
     }
     // round q takes the cluster's tiles from the last ones on; only round 0 may have tiles past T
     auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
-    const int q0 = tile_of(0) < tiles ? 0 : 1;
-    auto issue = [&](int q) {
-        if (q >= rounds) return;
-        const int t0 = tile_of(q) * L, sb = (q - q0) % kStages;
-        mbar_arrive_expect_tx(&sm.bar_a, (uint32_t)(L * 2 * kW * sizeof(T)));
-        tma_load_4d(sm.pr, &maps.pr, &sm.bar_a, d0, 0, t0, (int)b);
-        tma_load_4d(sm.g, &maps.g, &sm.bar_a, d0, 0, t0, (int)b);
-        mbar_arrive_expect_tx(&sm.bar_b[sb], (uint32_t)(L * 2 * kW * sizeof(T)));
-        tma_load_4d(sm.ix[sb], &maps.ix, &sm.bar_b[sb], d0, 1, t0, (int)b);
+    const int q0 = tile_of(0) < tiles ? 0 : 1;  // the block's first tile is of this round
+    auto issue_a = [&](int i) {
+        if (q0 + i >= rounds) return;
+        const int t0 = tile_of(q0 + i) * L, st = i % kA;
+        mbar_arrive_expect_tx(&sm.bar_a[st], (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.pr[st], &maps.pr, &sm.bar_a[st], d0, 0, t0, b);
+        tma_load_4d(sm.g[st], &maps.g, &sm.bar_a[st], d0, 0, t0, b);
     };
-    if (kTma && tid == 0) issue(q0);
+    auto issue_b = [&](int i) {
+        if (q0 + i >= rounds) return;
+        const int t0 = tile_of(q0 + i) * L, st = i % kB;
+        mbar_arrive_expect_tx(&sm.bar_b[st], (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.ix[st], &maps.ix, &sm.bar_b[st], d0, 1, t0, b);
+    };
+    if (kTma && tid == 0) {
+        for (int i = 0; i < kA; ++i) issue_a(i);
+        for (int i = 0; i < kB; ++i) issue_b(i);
+    }
     auto marks_of = [&](int q) -> unsigned {
         if (q >= rounds) return 0u;
-        const int64_t t = (int64_t)tile_of(q) * L + warp * R + lane;
-        return (pr.reset && lane < R && t < pr.T) ? pr.reset[row0 + t] : 0u;
+        const int t = tile_of(q) * L + warp * R + lane;
+        return (lane < R && t < T_) ? pr.reset[(int64_t)b * T_ + t] : 0u;
     };
-    unsigned mark = marks_of(0);
-    bool late = false, timeout = false;
-    f2 chk{0.0f, 0.0f}, sum{0.0f, 0.0f};
+    unsigned mark = kCuts ? marks_of(0) : 0u;
+    bool late = false;
+    f2 sum{0.0f, 0.0f}, chk{0.0f, 0.0f};
+
+    auto put = [&](T* o, f2 dpr, f2 dpi, f2 dx) {
+        if constexpr (kTma) {
+            if (in0) {
+                st2(o, dpr);
+                st2(o + D, dpi);
+                st2(o + 2 * D, dx);
+            }
+        } else {
+            if (in0) o[0] = to_out<T>(dpr.x), o[D] = to_out<T>(dpi.x), o[2 * D] = to_out<T>(dx.x);
+            if (in1) o[1] = to_out<T>(dpr.y), o[D + 1] = to_out<T>(dpi.y), o[2 * D + 1] = to_out<T>(dx.y);
+        }
+    };
 
     for (int q = 0; q < rounds; ++q) {
-        const int par = q & 1, n_in = q - q0, sb = kTma ? n_in % kStages : 0;
+        const int par = q & 1, i = q - q0;
         const int tile0 = tile_of(q) * L, t0 = tile0 + warp * R;
-        const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
-        mark = marks_of(q + 1);
-        const bool live = q >= q0;
-        const int n = live ? (int)max((int64_t)0, min((int64_t)R, pr.T - t0)) : 0;  // this warp's steps
-        if (live) {
+        const int n = max(0, min(R, T_ - t0));  // this warp's steps
+        const int sa = kTma && i >= 0 ? i % kA : 0, sb = kTma && i >= 0 ? i % kB : 0;
+        unsigned marks = 0;
+        if constexpr (kCuts) {
+            marks = __ballot_sync(0xffffffffu, mark != 0);
+            mark = marks_of(q + 1);
+        }
+        if (i >= 0) {
             if constexpr (kTma) {
-                timeout |= !wait_stage(&sm.bar_a, n_in & 1, late);
+                wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
             } else {
                 __syncthreads();  // the tile before has been read
-                for (int i = tid; i < L * 4 * kW; i += kNW * 32) {
-                    const int row = i / (4 * kW), g = (i / kW) % 4, c = i % kW;
-                    const int64_t t = tile0 + row;
+                for (int c4 = tid; c4 < L * 4 * kW; c4 += kNW * 32) {
+                    const int row = c4 / (4 * kW), g = (c4 / kW) % 4, c = c4 % kW, t = tile0 + row;
                     T val = T(0.0f);
-                    if (t < pr.T && d0 + c < pr.D) val = g < 3 ? px[(t * 3 + g) * pr.D + d0 + c] : dH[t * pr.D + d0 + c];
-                    T* to = g == 0 ? &sm.pr[row][c] : g == 3 ? &sm.g[row][c] : &sm.ix[0][row][g - 1][c];
+                    if (t < T_ && d0 + c < D)
+                        val = g < 3 ? px[((int64_t)t * 3 + g) * D + d0 + c] : dH[(int64_t)t * D + d0 + c];
+                    T* to = g == 0 ? &sm.pr[0][row][c] : g == 3 ? &sm.g[0][row][c] : &sm.ix[0][row][g - 1][c];
                     *to = val;
                 }
                 __syncthreads();
             }
         }
-        // pass 1: z, g and the element of mu over the warp's steps
-        f2 z[R], l[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            z[j] = l[j] = splat2(0.0f);
-            if (j < n) {
-                z[j] = mul2(khalf, sigmoid2(ld2(&sm.pr[warp * R + j][2 * lane])));
-                l[j] = ld2(&sm.g[warp * R + j][2 * lane]);
-            }
-        }
+        // y, g and the element of mu over the warp's steps; steps past T keep mu (y = 0, g = 0)
+        f2 y[R], l[R];
         Elem e{splat2(1.0f), splat2(0.0f)};
-        auto compose = [&](auto w) {
+        if (n == R && (!kCuts || marks == 0) && !wide) {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
+                y[j] = mul2(k, sigmoid_pair(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
+                l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
                 f2 a, m;
-                decay2<decltype(w)::value>(z[j], a, m);
+                decay2<false>(y[j], a, m);
                 e.B = mul2(a, add2(l[j], e.B));
                 e.P = mul2(a, e.P);
-                if (marks >> j & 1) e.B = splat2(0.0f);
             }
-        };
-        if (wide)
-            compose(std::true_type{});
-        else
-            compose(std::false_type{});
-        st2(&sm.warp[par][warp].P[2 * lane], e.P);
-        st2(&sm.warp[par][warp].B[2 * lane], e.B);
-        if (lane == 0) sm.warp_new[par][warp] = marks;
+        } else {
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                y[j] = l[j] = splat2(0.0f);
+                if (j < n) {
+                    y[j] = mul2(k, sigmoid_pair(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
+                    l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
+                    f2 a, m;
+                    decay2<true>(y[j], a, m);
+                    e.B = (marks >> j & 1) ? splat2(0.0f) : mul2(a, add2(l[j], e.B));
+                    e.P = mul2(a, e.P);
+                }
+            }
+            if (marks) e.P = splat2(-1.0f);
+        }
+        sm.warp[par][warp][lane] = pack(e);
         __syncthreads();
-        if (kTma && live && tid == 0) issue(q + 1);
-
+        if (kTma && tid == 0 && i >= 0) {
+            // this round's p_r and g have been read, and the round before is finished
+            issue_a(i + kA);
+            if (i >= 1) issue_b(i - 1 + kB);
+        }
         f2 mu;
         if constexpr (kCluster) {
-            Elem pre{splat2(1.0f), splat2(0.0f)}, all = pre;
-            unsigned pre_new = 0, all_new = 0;
-#pragma unroll
-            for (int w = kNW - 1; w >= 0; --w) {
-                if (w == warp) pre = all, pre_new = all_new;
-                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
-                const unsigned nw = sm.warp_new[par][w];
-                all.B = nw ? B : fma2(P, all.B, B);
-                all.P = mul2(P, all.P);
-                all_new |= nw;
+            Elem pre{splat2(1.0f), splat2(0.0f)};
+            for (int w = kNW - 1; w > warp; --w) pre = then<kCuts>(pre, unpack(sm.warp[par][w][lane]));
+            if (warp == 0) {
+                const float4 all = pack(then<kCuts>(pre, e));
+                for (int r = 0; r < C; ++r) send16(&sm.rank[par][rank][lane], &sm.rank_bar[par], r, all);
             }
-            for (int r = warp; r < C; r += kNW) {
-                st2_cluster(&sm.rank[par][rank].P[2 * lane], r, all.P);
-                st2_cluster(&sm.rank[par][rank].B[2 * lane], r, all.B);
-                if (lane == 0) st1_cluster(&sm.rank_new[par][rank], r, all_new);
+            wait_bar<true>(&sm.rank_bar[par], (q >> 1) & 1, late);
+            if (tid == 0) mbar_arrive_expect_tx(&sm.rank_bar[par], C * (uint32_t)sizeof sm.rank[0][0]);
+            mu = ld2(&sm.carry[par][lane].x);
+            for (int r = C - 1; r > (int)rank; --r) mu = apply<kCuts>(unpack(sm.rank[par][r][lane]), mu);
+            if (warp == 0) {
+                f2 c = mu;
+                for (int r = (int)rank; r >= 0; --r) c = apply<kCuts>(unpack(sm.rank[par][r][lane]), c);
+                sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
-            cluster_arrive_release();
-            cluster_wait_acquire();
-            f2 c = carry, mine = carry;
-            for (int r = C - 1; r >= 0; --r) {
-                if (r == (int)rank) mine = c;
-                const f2 P = ld2(&sm.rank[par][r].P[2 * lane]), B = ld2(&sm.rank[par][r].B[2 * lane]);
-                c = sm.rank_new[par][r] ? B : fma2(P, c, B);
-            }
-            carry = c;
-            mu = pre_new ? pre.B : fma2(pre.P, mine, pre.B);
+            mu = apply<kCuts>(pre, mu);
         } else {
-            f2 c = carry;
-            mu = carry;
-#pragma unroll
-            for (int w = kNW - 1; w >= 0; --w) {
-                if (w == warp) mu = c;
-                const f2 P = ld2(&sm.warp[par][w].P[2 * lane]), B = ld2(&sm.warp[par][w].B[2 * lane]);
-                c = sm.warp_new[par][w] ? B : fma2(P, c, B);
+            mu = ld2(&sm.carry[par][lane].x);
+            for (int w = kNW - 1; w > warp; --w) mu = apply<kCuts>(unpack(sm.warp[par][w][lane]), mu);
+            if (warp == 0) {
+                const f2 c = apply<kCuts>(e, mu);
+                sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
-            carry = c;
         }
-        if (kTma && live) timeout |= !wait_stage(&sm.bar_b[sb], (n_in / kStages) & 1, late);
+        if (kTma && i >= 0) wait_bar<false>(&sm.bar_b[sb], (i / kB) & 1, late);
         if (n == 0) continue;
-        // pass 2: l backwards, then the gradients forwards from the checkpoint
-        f2 h{0.0f, 0.0f};
-        const float* ck = pr.ck + (b * pr.nCk + t0 / R) * pr.D + d;
+        // l backwards from mu, then the gradients forwards from the checkpoint
+        f2 h{0.0f, 0.0f}, part{0.0f, 0.0f}, dpr, dpi, dx, w;
+        const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
         if (in0) h.x = ck[0];
         if (in1) h.y = ck[1];
-        T* o = dpx + (int64_t)t0 * 3 * pr.D;
-        f2 part{0.0f, 0.0f};
-        auto finish = [&](auto w) {
-            constexpr bool kWide = decltype(w)::value;
+        const T* p = &sm.ix[sb][warp * R][0][2 * lane];
+        T* o = static_cast<T*>(pr.dpx) + ((int64_t)b * T_ + t0) * 3 * D + d;
+        if (kTma && !wide && (!kCuts || marks == 0) && n == R) {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 f2 a, m;
-                decay2<kWide>(z[j], a, m);
+                decay2<false>(y[j], a, m);
                 l[j] = add2(l[j], mu);
                 mu = mul2(a, l[j]);
-                if (marks >> j & 1) mu = splat2(0.0f);
             }
-            const T* s = &sm.ix[sb][warp * R][0][2 * lane];
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                grads2<false>(y[j], l[j], ld2(p + j * 2 * kW), ld2(p + (j * 2 + 1) * kW), kinv, h, dpr, dpi, dx, w);
+                part = add2(part, w);
+                chk = fma2(dx, splat2(0.0f), chk);
+                put(o, dpr, dpi, dx);
+                o += 3 * D;
+            }
+        } else {
+#pragma unroll
+            for (int j = R - 1; j >= 0; --j) {
+                f2 a, m;
+                decay2<true>(y[j], a, m);
+                l[j] = add2(l[j], mu);
+                mu = (marks >> j & 1) ? splat2(0.0f) : mul2(a, l[j]);
+            }
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 if (j < n) {
-                    // evaluated again from z: a and m of all R steps would not stay in registers
-                    asm volatile("" : "+f"(z[j].x), "+f"(z[j].y));
-                    f2 dpr, dpi, dx, ww;
-                    grads2<kWide>(z[j], l[j], ld2(s + j * 2 * kW), ld2(s + (j * 2 + 1) * kW), kinv, marks >> j & 1, h, dpr,
-                                  dpi, dx, ww);
-                    part = add2(part, ww);
+                    if (marks >> j & 1) h = splat2(0.0f);
+                    grads2<true>(y[j], l[j], ld2(p + j * 2 * kW), ld2(p + (j * 2 + 1) * kW), kinv, h, dpr, dpi, dx, w);
+                    part = add2(part, w);
                     chk = fma2(dx, splat2(0.0f), chk);
-                    if constexpr (kTma) {
-                        if (in0) {
-                            st2(o, dpr);
-                            st2(o + pr.D, dpi);
-                            st2(o + 2 * pr.D, dx);
-                        }
-                    } else {
-                        if (in0) o[0] = to_out<T>(dpr.x), o[pr.D] = to_out<T>(dpi.x), o[2 * pr.D] = to_out<T>(dx.x);
-                        if (in1) o[1] = to_out<T>(dpr.y), o[pr.D + 1] = to_out<T>(dpi.y), o[2 * pr.D + 1] = to_out<T>(dx.y);
-                    }
+                    put(o, dpr, dpi, dx);
                 }
-                o += 3 * pr.D;
+                o += 3 * D;
             }
-        };
-        if (wide)
-            finish(std::true_type{});
-        else
-            finish(std::false_type{});
+        }
         sum = add2(sum, part);
         if (t0 == 0 && pr.dh0) {
-            float* q = pr.dh0 + b * pr.D + d;
-            if (in0) q[0] = mu.x;
-            if (in1) q[1] = mu.y;
+            float* to = pr.dh0 + (int64_t)b * D + d;
+            if (in0) to[0] = mu.x;
+            if (in1) to[1] = mu.y;
         }
     }
     // the warps' sums of w in order; a sum that is not finite stands for a dL/dp_r that is not
-    st2(&sm.sum[warp][2 * lane], sum);
+    __syncthreads();  // the last round's elements have been read
+    sm.warp[0][warp][lane] = make_float4(sum.x, sum.y, 0.0f, 0.0f);
     __syncthreads();
-    if (tid < kW && d0 + tid < pr.D) {
-        float s = 0.0f;
+    if (warp == 0) {
+        f2 t{0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < kNW; ++w) s += sm.sum[w][tid];
-        pr.part[(b * C + rank) * pr.D + d0 + tid] = s;
+        for (int w = 0; w < kNW; ++w) t = add2(t, unpack(sm.warp[0][w][lane]).P);
+        float* o = pr.part + ((int64_t)b * C + rank) * D + d;
+        if (in0) o[0] = t.x;
+        if (in1) o[1] = t.y;
     }
     chk = fma2(sum, splat2(0.0f), chk);
     const bool bad = (in0 && chk.x != chk.x) || (in1 && chk.y != chk.y);
     const unsigned bits = (__any_sync(0xffffffffu, bad) ? kStatusNonFinite : 0u) |
-                          (__any_sync(0xffffffffu, timeout) ? kStatusTimeout : 0u);
+                          (__any_sync(0xffffffffu, late) ? kStatusTimeout : 0u);
     if (bits && lane == 0) atomicOr(pr.status, bits);
+    if constexpr (kCluster) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
 }
 
 // dL/dlambda = sig(lambda) / softplus(lambda) * the sum of the blocks' partial
@@ -746,12 +790,11 @@ bool bad_sizes(int64_t B, int64_t T, int64_t D) {
     return B < 0 || T < 0 || D < 0 || B >= (int64_t(1) << 31) || T > (int64_t(1) << 30) || B * T >= (int64_t(1) << 31) ||
            D >= (int64_t(1) << 31) || (double)B * T * D > 4.0e12 || (double)B * D > 1.0e11;
 }
-int64_t n_checkpoints(int64_t T, pararnn_dtype dt) {
-    const int s = dt == PARARNN_F32 ? Ck<float>::kSteps : Ck<bf16>::kSteps;
-    return (T + s - 1) / s;
-}
+int64_t n_checkpoints(int64_t T) { return (T + kCkSteps - 1) / kCkSteps; }
 
 // ---- launches -------------------------------------------------------------------
+namespace {
+
 // Blocks per cluster: the smallest power of two that fills the device's SMs twice
 // (two blocks are resident per SM), as far as there are tiles for them.
 int ranks_for(int64_t groups, int64_t tiles, int sms) {
@@ -767,9 +810,7 @@ bool prepare_kernel(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return false;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
     done.fetch_or(bit, std::memory_order_release);
     return true;
 }
@@ -807,13 +848,26 @@ pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int
                                                                   : abi::cuda_fail(who, "kernel launch failed");
 }
 
+// calls f with three truth values as types
+template <class F>
+void choose(bool a, bool b, bool c, F f) {
+    auto two = [&](auto x, auto y) { c ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
+    auto one = [&](auto x) { b ? two(x, std::true_type{}) : two(x, std::false_type{}); };
+    a ? one(std::true_type{}) : one(std::false_type{});
+}
+
+// two blocks share an SM's 228 KB, of which each gives 1 KB to the system
+constexpr size_t kHalfSm = (228 * 1024) / 2 - 1024;
+static_assert(sizeof(FwdSmem<float>) + 128 <= kHalfSm && sizeof(FwdSmem<bf16>) + 128 <= kHalfSm, "two blocks per SM");
+static_assert(sizeof(BwdSmem<float>) + 128 <= kHalfSm && sizeof(BwdSmem<bf16>) + 128 <= kHalfSm, "two blocks per SM");
+
 template <typename T>
 pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
     constexpr int L = Tile<T>::L;
-    pr.nCG = (pr.D + kW - 1) / kW;
-    pr.nCk = n_checkpoints(pr.T, sizeof(T) == 4 ? PARARNN_F32 : PARARNN_BF16);
+    pr.nCG = (int)((pr.D + kW - 1) / kW);
+    pr.nCk = (int)n_checkpoints(pr.T);
     const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
     pr.ranks = ranks_for(groups, tiles, sms);
     if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
@@ -831,12 +885,10 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
     const size_t smem = sizeof(BwdSmem<T>) + 128;
     const int64_t blocks = groups * pr.ranks;
     pararnn_status s;
-    if (pr.ranks > 1)
-        s = tma ? launch_clusters<backward_kernel<T, true, true>>(who, pr, maps, blocks, pr.ranks, smem, st)
-                : launch_clusters<backward_kernel<T, false, true>>(who, pr, maps, blocks, pr.ranks, smem, st);
-    else
-        s = tma ? launch_clusters<backward_kernel<T, true, false>>(who, pr, maps, blocks, 1, smem, st)
-                : launch_clusters<backward_kernel<T, false, false>>(who, pr, maps, blocks, 1, smem, st);
+    choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
+        s = launch_clusters<backward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>>(
+            who, pr, maps, blocks, pr.ranks, smem, st);
+    });
     if (s != PARARNN_OK || !dlam) return s;
     dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.ranks, pr.D);
     return abi::launched(who);
@@ -846,27 +898,30 @@ template <typename T>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
-    pr.nCG = (pr.D + kW - 1) / kW;
-    pr.nCk = n_checkpoints(pr.T, sizeof(T) == 4 ? PARARNN_F32 : PARARNN_BF16);
-    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + Tile<T>::L - 1) / Tile<T>::L;
+    constexpr int L = Tile<T>::L;
+    pr.nCG = (int)((pr.D + kW - 1) / kW);
+    pr.nCk = (int)n_checkpoints(pr.T);
+    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
     pr.ranks = ranks_for(groups, tiles, sms);
     if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
     const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16);
     CUtensorMap map;
     memset(&map, 0, sizeof map);
     if (tma) {
-        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, Tile<T>::L);
+        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, L);
         if (s != PARARNN_OK) return s;
     }
     const size_t smem = sizeof(FwdSmem<T>) + 128;
     const int64_t blocks = groups * pr.ranks;
-    if (pr.ranks > 1)
-        return tma ? launch_clusters<forward_kernel<T, true, true>>(who, pr, map, blocks, pr.ranks, smem, st)
-                   : launch_clusters<forward_kernel<T, false, true>>(who, pr, map, blocks, pr.ranks, smem, st);
-    return tma ? launch_clusters<forward_kernel<T, true, false>>(who, pr, map, blocks, 1, smem, st)
-               : launch_clusters<forward_kernel<T, false, false>>(who, pr, map, blocks, 1, smem, st);
+    pararnn_status s;
+    choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
+        s = launch_clusters<forward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>>(
+            who, pr, map, blocks, pr.ranks, smem, st);
+    });
+    return s;
 }
 
+}  // namespace
 }  // namespace gs
 }  // namespace pararnn
 
@@ -876,12 +931,12 @@ extern "C" {
 
 size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype) {
     if (gs::bad_sizes(B, T, D) || abi::bad_dtype(dtype)) return 0;
-    return (size_t)(B * gs::n_checkpoints(T, dtype) * D) * sizeof(float);
+    return (size_t)(B * gs::n_checkpoints(T) * D) * sizeof(float);
 }
 
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D) {
     if (gs::bad_sizes(B, T, D)) return 0;
-    // a partial sum of dL/dlambda from each block of a cluster of up to 16
+    // a partial sum of dL/dlambda from each block of a cluster of up to 8
     return kHeaderBytes + (size_t)(B * D) * gs::kMaxRanks * sizeof(float);
 }
 

@@ -114,13 +114,15 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // mbarrier counts the bytes: no block waits for more than the data it needs.
 // Every pre-activation is read once, by tensor copies two or more tiles ahead.
 constexpr int kW = 64;  // channels per block
-constexpr int kNW = 8;  // warps per block
 constexpr int kMaxRanks = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <typename T>
+template <typename T, bool kForward>
 struct Tile {
-    static constexpr int R = kCkSteps, L = kNW * R;
+    // the forward of bfloat16 has the registers and the stages for 16 steps a thread
+    static constexpr int R = kForward && sizeof(T) == 2 ? 16 : kCkSteps;
+    static constexpr int NW = 8;  // warps per block
+    static constexpr int L = NW * R;
 };
 
 // An affine map h -> P h + B of two channels.  P is a product of decays, 0 to
@@ -147,9 +149,9 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
 
 template <typename T>
 struct FwdSmem {
-    static constexpr int kStages = 8 / sizeof(T);
-    alignas(128) T px[kStages][Tile<T>::L][3][kW];
-    float4 warp[2][kNW][32];        // each warp's element, two rounds in turn
+    static constexpr int kStages = 2;
+    alignas(128) T px[kStages][Tile<T, true>::L][3][kW];
+    float4 warp[2][Tile<T, true>::NW][32];  // each warp's element, two rounds in turn
     float4 rank[2][kMaxRanks][32];  // each of the cluster's tiles
     float2 carry[2][32];            // the state before the round
     uint64_t bar[kStages], rank_bar[2];
@@ -205,7 +207,9 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& l
 // at most 2.4e-8 of it with its coefficients in float32, and a is 1 - m, rounded
 // to nearest: an error of a that leans to one side would add up over a memory of 1/m
 // steps.  kWide, for decays that reach past 1: there a is the exponential, which keeps the
-// digits of a small a.
+// digits of a small a.  kTiny keeps 1 - a^2 above zero where y is zero (its root, 3e-19,
+// stands for zero then).
+constexpr float kTiny = 1e-37f;
 template <bool kWide>
 __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
     f2 s = fma2(y, splat2(1.29076303e-4f), splat2(-1.30077498e-3f));
@@ -214,7 +218,7 @@ __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
     s = fma2(y, s, splat2(1.66663408e-1f));
     s = fma2(y, s, splat2(-4.99999791e-1f));
     s = fma2(y, s, splat2(1.0f));
-    m = mul2(y, s);
+    m = fma2(y, s, splat2(kTiny));
     a = sub2(splat2(1.0f), m);
     if constexpr (kWide) {
         const f2 e = ex2_2(mul2(y, splat2(-kLog2e)));
@@ -225,34 +229,44 @@ __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
 }
 __device__ __forceinline__ f2 exp_neg2(f2 x) { return ex2_2(mul2(x, splat2(-kLog2e))); }
 
-// sig of two channels with one reciprocal (simultaneous inversion, as in inv_pair):
-// the special-function unit, 16 lanes a cycle and SM, is what the evaluation is
-// bound by.  Where the product of the denominators nears the float range each has its own.
-__device__ __forceinline__ f2 sigmoid_pair(f2 x) {
-    const f2 d = add2(exp_neg2(x), splat2(1.0f));
-    const float p = d.x * d.y, q = rcp_approx(p);
-    f2 r{d.y * q, d.x * q};
-    if (!(p <= 1e37f)) r = rcp_2(d);
+// y = k sig(p) of a channel in two steps with one reciprocal (simultaneous inversion,
+// as in inv_pair): the special-function unit, 16 lanes a cycle and SM, is the
+// busiest one.  `most` collects the largest product of two denominators: past
+// kProduct the reciprocal leaves the float range and the steps are evaluated again with
+// a reciprocal each.
+constexpr float kProduct = 1e37f;
+__device__ __forceinline__ void decay_exponents(f2 p0, f2 p1, f2 k, f2& y0, f2& y1, float& most) {
+    const f2 d0 = add2(exp_neg2(p0), splat2(1.0f)), d1 = add2(exp_neg2(p1), splat2(1.0f));
+    const f2 p = mul2(d0, d1);
+    const f2 q = mul2(k, rcp_2(p));
+    most = fmaxf(most, fmaxf(p.x, p.y));
+    y0 = mul2(d1, q);
+    y1 = mul2(d0, q);
+}
+// sig of two channels with one reciprocal and capped exponents, for a factor whose rounding below 2^-62 to 2^-62 does not show
+__device__ __forceinline__ f2 sigmoid_pair_capped(f2 x) {
+    const f2 d = sig_den2(x);
+    f2 r;
+    inv_pair(d.x, d.y, r.x, r.y);
     return r;
 }
 
-// a and u = sqrt(1 - a^2) sig(p_i) x.  With v = 1 - a^2 = m (1 + a) and d = 1 + e^{-p_i},
+// a and u = sqrt(1 - a^2) sig(p_i) x from y.  With v = 1 - a^2 = m (1 + a) and d = 1 + e^{-p_i},
 // u = x v / sqrt(v d^2): one reciprocal square root for the root and the gate's reciprocal.
-// An infinite d gives u = 0; the addend keeps v d^2 above zero where v = 0.
+// An infinite d gives u = 0.
 template <bool kWide>
-__device__ __forceinline__ void eval2(f2 pr, f2 pi, f2 x, f2 k, f2& a, f2& u) {
-    const f2 y = mul2(k, sigmoid_pair(pr));
+__device__ __forceinline__ void eval2(f2 y, f2 pi, f2 x, f2& a, f2& u) {
     f2 m;
     decay2<kWide>(y, a, m);
     const f2 v = fma2(m, a, m);
     const f2 d = add2(exp_neg2(pi), splat2(1.0f));
-    const f2 q = mul2(mul2(add2(v, splat2(1e-37f)), d), d);
+    const f2 q = mul2(mul2(v, d), d);
     u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
 }
 
 template <typename T, bool kTma, bool kCluster, bool kCuts>
-__global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
-    constexpr int kStages = FwdSmem<T>::kStages, R = Tile<T>::R, L = Tile<T>::L;
+__global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
+    constexpr int kStages = FwdSmem<T>::kStages, R = Tile<T, true>::R, L = Tile<T, true>::L, kNW = Tile<T, true>::NW;
     extern __shared__ unsigned char raw[];
     FwdSmem<T>& sm = *reinterpret_cast<FwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31;
@@ -307,6 +321,11 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
     };
     unsigned mark = kCuts ? marks_of(0) : 0u;
     bool late = false, bad = false;
+    auto keep = [&](int i, f2 h) {
+        float* o = pr.ck + ((int64_t)b * pr.nCk + i) * D + d;
+        if (in0) o[0] = h.x;
+        if (in1) o[1] = h.y;
+    };
     int t0 = (int)rank * L + warp * R;  // the warp's first step
     T* H = static_cast<T*>(pr.H) + ((int64_t)b * T_ + t0) * D;
 
@@ -332,14 +351,21 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
         Elem e{splat2(1.0f), splat2(0.0f)};
         if (t0 < T_) {
             const T* p = &sm.px[st][warp * R][0][2 * lane];
-            if (wide) {
+            float most = 0.0f;
+            if (!wide) {
+#pragma unroll
+                for (int j = 0; j < R; j += 2) {
+                    f2 y0, y1;
+                    decay_exponents(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 3) * kW), k, y0, y1, most);
+                    eval2<false>(y0, ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), a[j], u[j]);
+                    eval2<false>(y1, ld2(p + (j * 3 + 4) * kW), ld2(p + (j * 3 + 5) * kW), a[j + 1], u[j + 1]);
+                }
+            }
+            if (wide || __any_sync(0xffffffffu, most > kProduct)) {
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    eval2<true>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), k, a[j], u[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-                    eval2<false>(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), k, a[j], u[j]);
+                    eval2<true>(mul2(k, sigmoid2(ld2(p + j * 3 * kW))), ld2(p + (j * 3 + 1) * kW),
+                                ld2(p + (j * 3 + 2) * kW), a[j], u[j]);
             }
             e = Elem{a[0], u[0]};
             if (!kCuts || marks == 0) {
@@ -361,7 +387,12 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
         f2 h;
         if constexpr (kCluster) {
             Elem pre{splat2(1.0f), splat2(0.0f)};
-            for (int w = 0; w < warp; ++w) pre = then<kCuts>(pre, unpack(sm.warp[par][w][lane]));
+            float4 of[kNW - 1];
+#pragma unroll
+            for (int w = 0; w < kNW - 1; ++w) of[w] = sm.warp[par][w][lane];
+#pragma unroll
+            for (int w = 0; w < kNW - 1; ++w)
+                if (w < warp) pre = then<kCuts>(pre, unpack(of[w]));
             if (warp == kNW - 1) {
                 const float4 all = pack(then<kCuts>(pre, e));
                 for (int r = 0; r < C; ++r) send16(&sm.rank[par][rank][lane], &sm.rank_bar[par], r, all);
@@ -378,23 +409,27 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
             h = apply<kCuts>(pre, h);
         } else {
             h = ld2(&sm.carry[par][lane].x);
-            for (int w = 0; w < warp; ++w) h = apply<kCuts>(unpack(sm.warp[par][w][lane]), h);
+            // the elements are read at once: the last warp, whose chain of them is the longest, is
+            // what the next block barrier waits for
+            float4 of[kNW - 1];
+#pragma unroll
+            for (int w = 0; w < kNW - 1; ++w) of[w] = sm.warp[par][w][lane];
+#pragma unroll
+            for (int w = 0; w < kNW - 1; ++w)
+                if (w < warp) h = apply<kCuts>(unpack(of[w]), h);
             if (warp == kNW - 1) {
                 const f2 c = apply<kCuts>(e, h);
                 sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
         }
         if (t0 < T_) {
-            if (pr.ck) {
-                float* o = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
-                if (in0) o[0] = h.x;
-                if (in1) o[1] = h.y;
-            }
+            if (pr.ck) keep(t0 / kCkSteps, h);
             const int n = min(R, T_ - t0);
             T* o = H + d;
             if (kTma && (!kCuts || marks == 0) && n == R) {
 #pragma unroll
                 for (int j = 0; j < R; ++j) {
+                    if (j && j % kCkSteps == 0 && pr.ck) keep((t0 + j) / kCkSteps, h);
                     h = fma2(a[j], h, u[j]);
                     if (in0) st2(o, h);
                     o += D;
@@ -403,6 +438,7 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
 #pragma unroll
                 for (int j = 0; j < R; ++j)
                     if (j < n) {
+                        if (j && j % kCkSteps == 0 && pr.ck) keep((t0 + j) / kCkSteps, h);
                         if (kCuts && (marks >> j & 1)) {
                             bad |= (in0 && !isfinite(h.x)) || (in1 && !isfinite(h.y));
                             h = u[j];
@@ -448,10 +484,10 @@ __global__ void __launch_bounds__(kNW * 32, 2) forward_kernel(const Params pr, c
 template <typename T>
 struct BwdSmem {
     static constexpr int kA = 4 / sizeof(T), kB = kA + 1;  // stages of p_r and g, of p_i and x
-    alignas(128) T pr[kA][Tile<T>::L][kW];
-    alignas(128) T g[kA][Tile<T>::L][kW];
-    alignas(128) T ix[kB][Tile<T>::L][2][kW];
-    float4 warp[2][kNW][32];
+    alignas(128) T pr[kA][Tile<T, false>::L][kW];
+    alignas(128) T g[kA][Tile<T, false>::L][kW];
+    alignas(128) T ix[kB][Tile<T, false>::L][2][kW];
+    float4 warp[2][Tile<T, false>::NW][32];
     float4 rank[2][kMaxRanks][32];
     float2 carry[2][32];
     uint64_t bar_a[kA], bar_b[kB], rank_bar[2];
@@ -467,10 +503,8 @@ __device__ __forceinline__ void grads2(f2 y, f2 l, f2 pi, f2 x, f2 kinv, f2& h, 
     f2 a, m;
     decay2<kWide>(y, a, m);
     const f2 v = fma2(m, a, m);
-    // 1 / b; the addend keeps the root's argument above zero, and where v = 0 so is y, which scales the result
-    const f2 va = add2(v, splat2(1e-37f));
-    const f2 i = sigmoid_pair(pi);
-    const f2 ib = mul2(f2{rsqrt_approx(va.x), rsqrt_approx(va.y)}, i);  // i / b
+    const f2 i = sigmoid_pair_capped(pi);
+    const f2 ib = mul2(f2{rsqrt_approx(v.x), rsqrt_approx(v.y)}, i);  // i / b
     const f2 e = mul2(ib, x);
     const f2 ah = mul2(a, h);
     dx = mul2(l, mul2(v, ib));
@@ -481,8 +515,8 @@ __device__ __forceinline__ void grads2(f2 y, f2 l, f2 pi, f2 x, f2 kinv, f2& h, 
 }
 
 template <typename T, bool kTma, bool kCluster, bool kCuts>
-__global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
-    constexpr int kA = BwdSmem<T>::kA, kB = BwdSmem<T>::kB, R = Tile<T>::R, L = Tile<T>::L;
+__global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
+    constexpr int kA = BwdSmem<T>::kA, kB = BwdSmem<T>::kB, R = Tile<T, false>::R, L = Tile<T, false>::L, kNW = Tile<T, false>::NW;
     extern __shared__ unsigned char raw[];
     BwdSmem<T>& sm = *reinterpret_cast<BwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31;
@@ -594,22 +628,29 @@ __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams p
         // y, g and the element of mu over the warp's steps; steps past T keep mu (y = 0, g = 0)
         f2 y[R], l[R];
         Elem e{splat2(1.0f), splat2(0.0f)};
-        if (n == R && (!kCuts || marks == 0) && !wide) {
+        const bool plain = kTma && n == R && (!kCuts || marks == 0) && !wide;
+        float most = 0.0f;
+        if (plain) {
+#pragma unroll
+            for (int j = 0; j < R; j += 2)
+                decay_exponents(ld2(&sm.pr[sa][warp * R + j][2 * lane]), ld2(&sm.pr[sa][warp * R + j + 1][2 * lane]), k, y[j],
+                                y[j + 1], most);
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                y[j] = mul2(k, sigmoid_pair(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
                 l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
                 f2 a, m;
                 decay2<false>(y[j], a, m);
                 e.B = mul2(a, add2(l[j], e.B));
                 e.P = mul2(a, e.P);
             }
-        } else {
+        }
+        if (!plain || __any_sync(0xffffffffu, most > kProduct)) {
+            e = Elem{splat2(1.0f), splat2(0.0f)};
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 y[j] = l[j] = splat2(0.0f);
                 if (j < n) {
-                    y[j] = mul2(k, sigmoid_pair(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
+                    y[j] = mul2(k, sigmoid2(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
                     l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
                     f2 a, m;
                     decay2<true>(y[j], a, m);
@@ -629,7 +670,12 @@ __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams p
         f2 mu;
         if constexpr (kCluster) {
             Elem pre{splat2(1.0f), splat2(0.0f)};
-            for (int w = kNW - 1; w > warp; --w) pre = then<kCuts>(pre, unpack(sm.warp[par][w][lane]));
+            float4 of[kNW];
+#pragma unroll
+            for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
+#pragma unroll
+            for (int w = kNW - 1; w > 0; --w)
+                if (w > warp) pre = then<kCuts>(pre, unpack(of[w]));
             if (warp == 0) {
                 const float4 all = pack(then<kCuts>(pre, e));
                 for (int r = 0; r < C; ++r) send16(&sm.rank[par][rank][lane], &sm.rank_bar[par], r, all);
@@ -646,7 +692,12 @@ __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams p
             mu = apply<kCuts>(pre, mu);
         } else {
             mu = ld2(&sm.carry[par][lane].x);
-            for (int w = kNW - 1; w > warp; --w) mu = apply<kCuts>(unpack(sm.warp[par][w][lane]), mu);
+            float4 of[kNW];
+#pragma unroll
+            for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
+#pragma unroll
+            for (int w = kNW - 1; w > 0; --w)
+                if (w > warp) mu = apply<kCuts>(unpack(of[w]), mu);
             if (warp == 0) {
                 const f2 c = apply<kCuts>(e, mu);
                 sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
@@ -661,7 +712,7 @@ __global__ void __launch_bounds__(kNW * 32, 2) backward_kernel(const BwdParams p
         if (in1) h.y = ck[1];
         const T* p = &sm.ix[sb][warp * R][0][2 * lane];
         T* o = static_cast<T*>(pr.dpx) + ((int64_t)b * T_ + t0) * 3 * D + d;
-        if (kTma && !wide && (!kCuts || marks == 0) && n == R) {
+        if (plain) {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 f2 a, m;
@@ -826,7 +877,7 @@ int sm_count() {
     return sms;
 }
 
-template <auto kern, class P, class Map>
+template <auto kern, int kThreadCount, class P, class Map>
 pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int64_t blocks, int ranks,
                                size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
@@ -834,7 +885,7 @@ pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3(kNW * 32, 1, 1);
+    cfg.blockDim = dim3(kThreadCount, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -865,7 +916,7 @@ template <typename T>
 pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
-    constexpr int L = Tile<T>::L;
+    constexpr int L = Tile<T, false>::L;
     pr.nCG = (int)((pr.D + kW - 1) / kW);
     pr.nCk = (int)n_checkpoints(pr.T);
     const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
@@ -886,7 +937,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
     const int64_t blocks = groups * pr.ranks;
     pararnn_status s;
     choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
-        s = launch_clusters<backward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>>(
+        s = launch_clusters<backward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>, Tile<T, false>::NW * 32>(
             who, pr, maps, blocks, pr.ranks, smem, st);
     });
     if (s != PARARNN_OK || !dlam) return s;
@@ -898,7 +949,7 @@ template <typename T>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
-    constexpr int L = Tile<T>::L;
+    constexpr int L = Tile<T, true>::L;
     pr.nCG = (int)((pr.D + kW - 1) / kW);
     pr.nCk = (int)n_checkpoints(pr.T);
     const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
@@ -915,7 +966,7 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const int64_t blocks = groups * pr.ranks;
     pararnn_status s;
     choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
-        s = launch_clusters<forward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>>(
+        s = launch_clusters<forward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>, Tile<T, true>::NW * 32>(
             who, pr, map, blocks, pr.ranks, smem, st);
     });
     return s;

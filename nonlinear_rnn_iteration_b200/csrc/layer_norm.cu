@@ -7,9 +7,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "abi_util.cuh"
 #include "common.cuh"
@@ -19,8 +21,6 @@ namespace pararnn {
 namespace ln {
 
 typedef __nv_bfloat16 bf16;
-constexpr int kThreads = 128;
-constexpr int kSplits = 64;  // row ranges whose column sums are formed apart
 
 struct Params {
     const void* x;
@@ -32,6 +32,8 @@ struct Params {
     unsigned* status;
     int64_t M, P, N;
     float eps;
+    int tpr;           // threads per row
+    int pb, gpp, npc;  // row slots of one block: pb of the P parameter rows, gpp positions each; ranges of P
 };
 struct BwdParams {
     const void* x;
@@ -40,83 +42,344 @@ struct BwdParams {
     const float* rstd;
     const void* dy;
     void* dx;
-    float* part;  // [kSplits][2][P * N]
+    float* part;  // [range of positions][2][P * N], or null
     unsigned* status;
     int64_t M, P, N;
+    int tpr, pb, gpp, npc;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// ---- rows in registers ----------------------------------------------------------
+// A row of N values belongs to `tpr` threads (a power of two), each with K vectors of V
+// values, read and written once.  A thread's rows all have the same p, so that it
+// keeps its weights, and in the backward pass its column sums, in registers over all
+// its rows; the next row is read while the present one is reduced.  Bound by
+// HBM; two reductions of a row in the forward pass (the variance is taken about the
+// mean), one of two sums in the backward pass.
+template <typename T, int V>
+struct Vec {
+    static constexpr int kWords = V * sizeof(T) / 4;
+    uint32_t r[kWords > 0 ? kWords : 1];
+};
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+    Vec<T, V> v;
+    if constexpr (V * sizeof(T) == 16) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        v.r[0] = q.x, v.r[1] = q.y, v.r[2] = q.z, v.r[3] = q.w;
+    } else if constexpr (V * sizeof(T) == 4) {
+        v.r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+        v.r[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
     return v;
 }
+template <typename T, int V>
+__device__ __forceinline__ float value(const Vec<T, V>& v, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(v.r[i]);
+    return __uint_as_float(i & 1 ? v.r[i / 2] & 0xffff0000u : v.r[i / 2] << 16);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float* v) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 4)
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            p[0] = v[0];
+    } else if constexpr (V == 1) {
+        p[0] = __float2bfloat16_rn(v[0]);
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (V == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+}
 
-// one warp per row
-template <typename T>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Params pr) {
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= pr.M * pr.P) return;
-    const T* x = static_cast<const T*>(pr.x) + row * pr.N;
-    T* y = static_cast<T*>(pr.y) + row * pr.N;
-    const int64_t at = (row % pr.P) * pr.N;
-    float s = 0.0f;
-    for (int64_t j = lane; j < pr.N; j += 32) s += PxTraits<T>::cvt(x[j]);
-    const float mean = warp_sum(s) / (float)pr.N;
-    s = 0.0f;
-    for (int64_t j = lane; j < pr.N; j += 32) {
-        const float c = PxTraits<T>::cvt(x[j]) - mean;
-        s = __fmaf_rn(c, c, s);
+// The sum of two values over a row's threads.  Rows of more than a warp meet in shared
+// memory, two buffers in turn; every thread of the block takes part.
+__device__ __forceinline__ float2 row_sum(float a, float b, int tpr, float2 (*buf)[32], int& turn) {
+    for (int o = min(tpr, 32) >> 1; o; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    const float rstd = 1.0f / sqrtf(warp_sum(s) / (float)pr.N + pr.eps);
-    bool bad = false;
-    for (int64_t j = lane; j < pr.N; j += 32) {
-        const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
-        const float v = __fmaf_rn(xh, pr.w ? pr.w[at + j] : 1.0f, pr.b ? pr.b[at + j] : 0.0f);
-        y[j] = to_out<T>(v);
-        bad |= !isfinite(v);
+    if (tpr > 32) {
+        const int warp = threadIdx.x >> 5, per = tpr >> 5;
+        if ((threadIdx.x & 31) == 0) buf[turn][warp] = make_float2(a, b);
+        __syncthreads();
+        const float2* q = buf[turn] + warp / per * per;
+        a = b = 0.0f;
+        for (int i = 0; i < per; ++i) a += q[i].x, b += q[i].y;
+        turn ^= 1;
     }
-    if (lane == 0 && pr.mean) pr.mean[row] = mean;
-    if (lane == 0 && pr.rstd) pr.rstd[row] = rstd;
-    if (bad && pr.status) atomicOr(pr.status, kStatusNonFinite);
+    return make_float2(a, b);
+}
+
+// the rows of this thread's group: m0, m0 + dm, ... below M with parameter row p
+struct Rows {
+    int64_t p, m0, dm;
+    int64_t turns;  // of the whole block
+    bool on;
+};
+template <class P>
+__device__ __forceinline__ Rows rows_of(const P& pr) {
+    const int g = threadIdx.x / pr.tpr;
+    const int64_t range = blockIdx.x % pr.npc, slot = blockIdx.x / pr.npc, slots = gridDim.x / pr.npc;
+    Rows r;
+    r.p = range * pr.pb + g % pr.pb;
+    r.m0 = slot * pr.gpp + g / pr.pb;
+    r.dm = slots * pr.gpp;
+    r.on = g < pr.pb * pr.gpp && r.p < pr.P;
+    r.turns = (pr.M - slot * pr.gpp + r.dm - 1) / r.dm;
+    return r;
+}
+
+template <typename T, int V, int K, bool kBig>
+__global__ void __launch_bounds__(kBig ? 1024 : 256) forward_rows(const Params pr) {
+    __shared__ float2 buf[2][32];
+    const Rows rows = rows_of(pr);
+    const int j0 = (threadIdx.x % pr.tpr) * V, dj = pr.tpr * V, N = (int)pr.N;
+    const float inv = 1.0f / (float)N;
+    int turn = 0;
+    float w[K * V], b[K * V], chk = 0.0f;
+    Vec<T, V> v[K], next[K];
+    const T* x = static_cast<const T*>(pr.x);
+    auto fetch = [&](int64_t m, Vec<T, V>* to) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            to[k] = Vec<T, V>{};
+            if (rows.on && m < pr.M && j0 + k * dj < N) to[k] = load<T, V>(x + (m * pr.P + rows.p) * N + j0 + k * dj);
+        }
+    };
+    auto params = [&]() {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int j = j0 + k * dj + i;
+                const bool in = rows.on && j < N;
+                w[k * V + i] = in && pr.w ? pr.w[rows.p * N + j] : 1.0f;
+                b[k * V + i] = in && pr.b ? pr.b[rows.p * N + j] : 0.0f;
+            }
+    };
+    fetch(rows.m0, v);
+    if (!kBig) params();
+    for (int64_t it = 0; it < rows.turns; ++it) {
+        const int64_t m = rows.m0 + it * rows.dm;
+        if (!kBig) fetch(m + rows.dm, next);
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += value<T, V>(v[k], i);
+        const float mean = row_sum(s, 0.0f, pr.tpr, buf, turn).x * inv;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (j0 + k * dj < N)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = value<T, V>(v[k], i) - mean;
+                    s = __fmaf_rn(c, c, s);
+                }
+        const float rstd = 1.0f / sqrtf(row_sum(s, 0.0f, pr.tpr, buf, turn).x * inv + pr.eps);
+        if (rows.on && m < pr.M) {
+            const int64_t row = m * pr.P + rows.p;
+            if (kBig) params();
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (j0 + k * dj < N) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        o[i] = __fmaf_rn((value<T, V>(v[k], i) - mean) * rstd, w[k * V + i], b[k * V + i]);
+                        chk = __fmaf_rn(o[i], 0.0f, chk);
+                    }
+                    store<T, V>(static_cast<T*>(pr.y) + row * N + j0 + k * dj, o);
+                }
+            if (j0 == 0 && pr.mean) pr.mean[row] = mean;
+            if (j0 == 0 && pr.rstd) pr.rstd[row] = rstd;
+        }
+        if (kBig) {
+            fetch(m + rows.dm, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = next[k];
+        }
+    }
+    if (chk != chk && pr.status) atomicOr(pr.status, kStatusNonFinite);
+}
+
+template <typename T, int V, int K, bool kBig>
+__global__ void __launch_bounds__(kBig ? 1024 : 256) backward_rows(const BwdParams pr) {
+    __shared__ float2 buf[2][32];
+    extern __shared__ float2 sums[];  // [K * V][threads]
+    const Rows rows = rows_of(pr);
+    const int j0 = (threadIdx.x % pr.tpr) * V, dj = pr.tpr * V, N = (int)pr.N;
+    const float inv = 1.0f / (float)N;
+    int turn = 0;
+    float w[K * V], dw[K * V], db[K * V], chk = 0.0f;
+    Vec<T, V> v[K], g[K], nv[K], ng[K];
+    float mean = 0.0f, rstd = 0.0f, nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t m, Vec<T, V>* x, Vec<T, V>* dy, float& mu, float& rs) {
+        const bool on = rows.on && m < pr.M;
+        const int64_t row = on ? m * pr.P + rows.p : 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k] = Vec<T, V>{};
+            dy[k] = Vec<T, V>{};
+            if (on && j0 + k * dj < N) {
+                x[k] = load<T, V>(static_cast<const T*>(pr.x) + row * N + j0 + k * dj);
+                dy[k] = load<T, V>(static_cast<const T*>(pr.dy) + row * N + j0 + k * dj);
+            }
+        }
+        mu = on ? pr.mean[row] : 0.0f;
+        rs = on ? pr.rstd[row] : 0.0f;
+    };
+    auto params = [&]() {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int j = j0 + k * dj + i;
+                w[k * V + i] = rows.on && j < N && pr.w ? pr.w[rows.p * N + j] : 1.0f;
+            }
+    };
+#pragma unroll
+    for (int e = 0; e < K * V; ++e) dw[e] = db[e] = 0.0f;
+    fetch(rows.m0, v, g, mean, rstd);
+    if (!kBig) params();
+    for (int64_t it = 0; it < rows.turns; ++it) {
+        const int64_t m = rows.m0 + it * rows.dm;
+        if (!kBig) fetch(m + rows.dm, nv, ng, nmean, nrstd);
+        if (kBig) params();
+        float s1 = 0.0f, s2 = 0.0f;
+        // the threads past N and the rows past M hold zeros: they add nothing but -mean * 0
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float dy = value<T, V>(g[k], i), xh = (value<T, V>(v[k], i) - mean) * rstd;
+                const float d = dy * w[k * V + i];
+                s1 += d;
+                s2 = __fmaf_rn(d, xh, s2);
+                if (j0 + k * dj < N) {
+                    db[k * V + i] += dy;
+                    dw[k * V + i] = __fmaf_rn(dy, xh, dw[k * V + i]);
+                }
+            }
+        const float2 t = row_sum(s1, s2, pr.tpr, buf, turn);
+        const float m1 = t.x * inv, m2 = t.y * inv;
+        if (rows.on && m < pr.M) {
+            T* o = static_cast<T*>(pr.dx) + (m * pr.P + rows.p) * N + j0;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (j0 + k * dj < N) {
+                    float q[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float xh = (value<T, V>(v[k], i) - mean) * rstd;
+                        q[i] = rstd * (__fmaf_rn(value<T, V>(g[k], i), w[k * V + i], -m1) - xh * m2);
+                        chk = __fmaf_rn(q[i], 0.0f, chk);
+                    }
+                    store<T, V>(o + k * dj, q);
+                }
+        }
+        if (kBig) {
+            fetch(m + rows.dm, v, g, mean, rstd);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = nv[k], g[k] = ng[k];
+            mean = nmean;
+            rstd = nrstd;
+        }
+    }
+    if (chk != chk) atomicOr(pr.status, kStatusNonFinite);
+    if (!pr.part) return;
+    // the block's column sums: the groups of one parameter row in order
+#pragma unroll
+    for (int e = 0; e < K * V; ++e) sums[e * blockDim.x + threadIdx.x] = make_float2(dw[e], db[e]);
+    __syncthreads();
+    const int g0 = threadIdx.x / pr.tpr;
+    if (g0 < pr.pb && rows.p < pr.P) {
+        float* to = pr.part + (int64_t)(blockIdx.x / pr.npc) * 2 * pr.P * N + rows.p * N;
+#pragma unroll
+        for (int e = 0; e < K * V; ++e) {
+            const int j = j0 + e / V * dj + e % V;
+            float2 t = make_float2(0.0f, 0.0f);
+            for (int q = 0; q < pr.gpp; ++q) {
+                const float2 u = sums[e * blockDim.x + threadIdx.x + q * pr.pb * pr.tpr];
+                t.x += u.x, t.y += u.y;
+            }
+            if (j < N) {
+                to[j] = t.x;
+                to[pr.P * N + j] = t.y;
+            }
+        }
+    }
+}
+
+// ---- rows of any length -----------------------------------------------------------
+// For rows that do not fit a block's registers: a block per row, which reads it
+// once for each sum; the column sums are formed by a kernel of their own.
+constexpr int kLongThreads = 512;
+
+__device__ __forceinline__ float2 block_sum(float a, float b) {
+    __shared__ float2 buf[kLongThreads / 32];
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLongThreads / 32; ++i) a += buf[i].x, b += buf[i].y;
+    return make_float2(a, b);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dx_kernel(const BwdParams pr) {
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= pr.M * pr.P) return;
-    const T* x = static_cast<const T*>(pr.x) + row * pr.N;
-    const T* dy = static_cast<const T*>(pr.dy) + row * pr.N;
-    T* dx = static_cast<T*>(pr.dx) + row * pr.N;
-    const int64_t at = (row % pr.P) * pr.N;
-    const float mean = pr.mean[row], rstd = pr.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t j = lane; j < pr.N; j += 32) {
-        const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
-        const float d = PxTraits<T>::cvt(dy[j]) * (pr.w ? pr.w[at + j] : 1.0f);
-        s1 += d;
-        s2 = __fmaf_rn(d, xh, s2);
+__global__ void __launch_bounds__(kLongThreads) forward_long(const Params pr) {
+    float chk = 0.0f;
+    for (int64_t row = blockIdx.x; row < pr.M * pr.P; row += gridDim.x) {
+        const T* x = static_cast<const T*>(pr.x) + row * pr.N;
+        T* y = static_cast<T*>(pr.y) + row * pr.N;
+        const int64_t at = (row % pr.P) * pr.N;
+        float s = 0.0f;
+        for (int64_t j = threadIdx.x; j < pr.N; j += kLongThreads) s += PxTraits<T>::cvt(x[j]);
+        const float mean = block_sum(s, 0.0f).x / (float)pr.N;
+        s = 0.0f;
+        for (int64_t j = threadIdx.x; j < pr.N; j += kLongThreads) {
+            const float c = PxTraits<T>::cvt(x[j]) - mean;
+            s = __fmaf_rn(c, c, s);
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f).x / (float)pr.N + pr.eps);
+        for (int64_t j = threadIdx.x; j < pr.N; j += kLongThreads) {
+            const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
+            const float v = __fmaf_rn(xh, pr.w ? pr.w[at + j] : 1.0f, pr.b ? pr.b[at + j] : 0.0f);
+            y[j] = to_out<T>(v);
+            chk = __fmaf_rn(v, 0.0f, chk);
+        }
+        if (threadIdx.x == 0 && pr.mean) pr.mean[row] = mean;
+        if (threadIdx.x == 0 && pr.rstd) pr.rstd[row] = rstd;
     }
-    const float m1 = warp_sum(s1) / (float)pr.N, m2 = warp_sum(s2) / (float)pr.N;
-    bool bad = false;
-    for (int64_t j = lane; j < pr.N; j += 32) {
-        const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
-        const float d = PxTraits<T>::cvt(dy[j]) * (pr.w ? pr.w[at + j] : 1.0f);
-        const float v = rstd * (d - m1 - xh * m2);
-        dx[j] = to_out<T>(v);
-        bad |= !isfinite(v);
-    }
-    if (bad) atomicOr(pr.status, kStatusNonFinite);
+    if (chk != chk && pr.status) atomicOr(pr.status, kStatusNonFinite);
 }
 
-// column sums of dy xh and dy over a range of the M positions
+// column sums of dy xh and dy over a range of the M positions: before dx, which may
+// be written over x or dy
 template <typename T>
-__global__ void __launch_bounds__(kThreads) columns_kernel(const BwdParams pr) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x, C = pr.P * pr.N;
+__global__ void __launch_bounds__(kLongThreads) columns_long(const BwdParams pr) {
+    const int64_t c = (int64_t)blockIdx.x * kLongThreads + threadIdx.x, C = pr.P * pr.N;
     if (c >= C) return;
     const int64_t p = c / pr.N;
-    const int64_t m0 = pr.M * blockIdx.y / kSplits, m1 = pr.M * (blockIdx.y + 1) / kSplits;
+    const int64_t m0 = pr.M * blockIdx.y / gridDim.y, m1 = pr.M * (blockIdx.y + 1) / gridDim.y;
     float sw = 0.0f, sb = 0.0f;
     for (int64_t m = m0; m < m1; ++m) {
         const float d = PxTraits<T>::cvt(static_cast<const T*>(pr.dy)[m * C + c]);
@@ -128,17 +391,194 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const BwdParams pr) {
     pr.part[(int64_t)blockIdx.y * 2 * C + C + c] = sb;
 }
 
-__global__ void reduce_kernel(const float* part, float* dw, float* db, int64_t C) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= C) return;
-    float sw = 0.0f, sb = 0.0f;
-    for (int q = 0; q < kSplits; ++q) {
-        sw += part[(int64_t)q * 2 * C + c];
-        sb += part[(int64_t)q * 2 * C + C + c];
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads) dx_long(const BwdParams pr) {
+    float chk = 0.0f;
+    for (int64_t row = blockIdx.x; row < pr.M * pr.P; row += gridDim.x) {
+        const T* x = static_cast<const T*>(pr.x) + row * pr.N;
+        const T* dy = static_cast<const T*>(pr.dy) + row * pr.N;
+        T* dx = static_cast<T*>(pr.dx) + row * pr.N;
+        const int64_t at = (row % pr.P) * pr.N;
+        const float mean = pr.mean[row], rstd = pr.rstd[row];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t j = threadIdx.x; j < pr.N; j += kLongThreads) {
+            const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
+            const float d = PxTraits<T>::cvt(dy[j]) * (pr.w ? pr.w[at + j] : 1.0f);
+            s1 += d;
+            s2 = __fmaf_rn(d, xh, s2);
+        }
+        const float2 t = block_sum(s1, s2);
+        const float m1 = t.x / (float)pr.N, m2 = t.y / (float)pr.N;
+        for (int64_t j = threadIdx.x; j < pr.N; j += kLongThreads) {
+            const float xh = (PxTraits<T>::cvt(x[j]) - mean) * rstd;
+            const float d = PxTraits<T>::cvt(dy[j]) * (pr.w ? pr.w[at + j] : 1.0f);
+            const float v = rstd * (d - m1 - xh * m2);
+            dx[j] = to_out<T>(v);
+            chk = __fmaf_rn(v, 0.0f, chk);
+        }
     }
-    if (dw) dw[c] = sw;
-    if (db) db[c] = sb;
+    if (chk != chk) atomicOr(pr.status, kStatusNonFinite);
 }
+
+// The blocks' partial sums added up: lane = column, each warp every sixteenth partial in order,
+// then the warps in order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) reduce_kernel(const float* part, int parts, float* dw, float* db,
+                                                                int64_t C) {
+    __shared__ float acc[kSumWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // of 2 C columns
+    float s = 0.0f;
+    if (c < 2 * C)
+#pragma unroll 4
+        for (int q = warp; q < parts; q += kSumWarps) s += part[(int64_t)q * 2 * C + c];
+    acc[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < 2 * C) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSumWarps; ++w) s += acc[w][lane];
+        float* to = c < C ? dw : db;
+        if (to) to[c < C ? c : c - C] = s;
+    }
+}
+
+// ---- launches -------------------------------------------------------------------
+// Partial sums of the columns that a backward call may use: at most this many, and at
+// most about 16 MB of them (one at least).
+constexpr int kMaxParts = 1184;
+int64_t max_parts(int64_t M, int64_t C) {
+    const int64_t fit = (int64_t(16) << 20) / (8 * C);
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(M, kMaxParts), fit));
+}
+
+namespace {
+
+struct Plan {
+    int vec, each;  // values per access and per thread; 0: rows of any length
+    bool big;
+    int tpr, threads, pb, gpp, npc;
+};
+
+int pow2_at_least(int64_t n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+// Values per thread: 8 as long as 256 threads hold the row, then 16, and past
+// 256 threads' registers blocks of up to 1024 threads that read the weights with each row.
+Plan plan_of(int64_t P, int64_t N, int esz, bool by16, bool by4) {
+    Plan p{};
+    p.vec = by16 ? 16 / esz : (esz == 2 && by4) ? 2 : 1;
+    if (N > 16384) return Plan{};
+    p.big = N > 4096;
+    p.each = N > 2048 ? 16 : 8;
+    p.tpr = pow2_at_least((N + p.each - 1) / p.each);
+    p.threads = p.big ? p.tpr : 256;
+    const int groups = p.threads / p.tpr;
+    p.pb = (int)std::min<int64_t>(P, groups);
+    p.gpp = groups / p.pb;
+    p.npc = (int)((P + p.pb - 1) / p.pb);
+    return p;
+}
+
+// calls f with the values per access, the accesses per thread and `big` as types
+template <typename T, class F>
+bool with_shape(const Plan& p, F f) {
+#define PARARNN_LN(V, E, B)                                                                                       \
+    if (p.vec == V && p.each == E && p.big == B) {                                                                \
+        f(std::integral_constant<int, V>{}, std::integral_constant<int, E / V>{}, std::integral_constant<bool, B>{}); \
+        return true;                                                                                              \
+    }
+#define PARARNN_LN_ALL(V) PARARNN_LN(V, 8, false) PARARNN_LN(V, 16, false) PARARNN_LN(V, 16, true)
+    if constexpr (sizeof(T) == 2) {
+        PARARNN_LN_ALL(8)
+        PARARNN_LN_ALL(2)
+    } else {
+        PARARNN_LN_ALL(4)
+    }
+    PARARNN_LN_ALL(1)
+#undef PARARNN_LN_ALL
+#undef PARARNN_LN
+    return false;
+}
+
+int sm_count() {
+    static thread_local int dev_of = -1, sms = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev != dev_of) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        dev_of = dev;
+    }
+    return sms;
+}
+
+// Blocks: as many as are resident at `threads_per_sm` threads per SM, or as there are rows
+// for; `slots` ranges of positions for each range of parameter rows.
+int64_t slots_for(const Plan& p, int64_t M, int sms, int threads_per_sm) {
+    const int64_t want = std::max<int64_t>(1, (int64_t)sms * (threads_per_sm / p.threads) / p.npc);
+    return std::max<int64_t>(1, std::min<int64_t>(want, (M + p.gpp - 1) / p.gpp));
+}
+
+template <typename T>
+pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
+    const bool by16 = (pr.N * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.x, 16) && !abi::misaligned(pr.y, 16);
+    const bool by4 = (pr.N * sizeof(T)) % 4 == 0 && !abi::misaligned(pr.x, 4) && !abi::misaligned(pr.y, 4);
+    const Plan p = plan_of(pr.P, pr.N, sizeof(T), by16, by4);
+    if (!p.vec) {
+        forward_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
+        return abi::launched(who);
+    }
+    pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
+    const int64_t blocks = slots_for(p, pr.M, sms, p.big ? 1024 : p.each == 16 ? 768 : 1024) * p.npc;
+    with_shape<T>(p, [&](auto v, auto k, auto big) {
+        forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>
+            <<<(unsigned)blocks, p.threads, 0, st>>>(pr);
+    });
+    return abi::launched(who);
+}
+
+template <typename T>
+pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* db, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
+    const int64_t C = pr.P * pr.N;
+    const bool sums = dw || db;
+    auto ok = [&](size_t a) {
+        return (pr.N * sizeof(T)) % a == 0 && !abi::misaligned(pr.x, a) && !abi::misaligned(pr.dy, a) &&
+               !abi::misaligned(pr.dx, a);
+    };
+    const Plan p = plan_of(pr.P, pr.N, sizeof(T), ok(16), ok(4));
+    if (!sums) pr.part = nullptr;
+    int64_t parts;
+    if (!p.vec) {
+        parts = std::min<int64_t>(max_parts(pr.M, C), 64);
+        const dim3 cols((unsigned)((C + kLongThreads - 1) / kLongThreads), (unsigned)parts);
+        if (sums) columns_long<T><<<cols, kLongThreads, 0, st>>>(pr);
+        dx_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
+    } else {
+        pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
+        parts = slots_for(p, pr.M, sms, p.big ? 1024 : 512);
+        if (sums) parts = std::min<int64_t>(parts, max_parts(pr.M, C));
+        with_shape<T>(p, [&](auto v, auto k, auto big) {
+            constexpr int each = decltype(v)::value * decltype(k)::value;
+            auto kern = backward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
+            const size_t smem = sums ? (size_t)each * p.threads * sizeof(float2) : 0;
+            if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            kern<<<(unsigned)(parts * p.npc), p.threads, smem, st>>>(pr);
+        });
+    }
+    const pararnn_status s = abi::launched(who);
+    if (s != PARARNN_OK || !sums) return s;
+    reduce_kernel<<<(unsigned)((2 * C + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, (int)parts, dw, db, C);
+    return abi::launched(who);
+}
+
+}  // namespace
 
 bool bad_sizes(int64_t M, int64_t P, int64_t N) {
     const int64_t lim = int64_t(1) << 31;
@@ -154,7 +594,7 @@ extern "C" {
 
 size_t pararnn_layer_norm_workspace_bytes(int64_t M, int64_t P, int64_t N) {
     if (ln::bad_sizes(M, P, N)) return 0;
-    return kHeaderBytes + (size_t)(P * N) * 2 * ln::kSplits * sizeof(float);
+    return kHeaderBytes + (size_t)(ln::max_parts(M, P * N) * P * N) * 2 * sizeof(float);
 }
 
 pararnn_status pararnn_layer_norm_forward(int64_t M, int64_t P, int64_t N, pararnn_dtype dtype, const void* x,
@@ -185,12 +625,7 @@ pararnn_status pararnn_layer_norm_forward(int64_t M, int64_t P, int64_t N, parar
     pr.P = P;
     pr.N = N;
     pr.eps = eps;
-    const unsigned grid = (unsigned)((M * P + 3) / 4);
-    if (dtype == PARARNN_F32)
-        ln::forward_kernel<float><<<grid, ln::kThreads, 0, st>>>(pr);
-    else
-        ln::forward_kernel<ln::bf16><<<grid, ln::kThreads, 0, st>>>(pr);
-    return abi::launched(who);
+    return dtype == PARARNN_F32 ? ln::launch_forward<float>(who, pr, st) : ln::launch_forward<ln::bf16>(who, pr, st);
 }
 
 pararnn_status pararnn_layer_norm_backward(int64_t M, int64_t P, int64_t N, pararnn_dtype dtype, const void* x,
@@ -229,20 +664,8 @@ pararnn_status pararnn_layer_norm_backward(int64_t M, int64_t P, int64_t N, para
     pr.M = M;
     pr.P = P;
     pr.N = N;
-    const int64_t C = P * N;
-    const unsigned grid = (unsigned)((M * P + 3) / 4);
-    const dim3 cols((unsigned)((C + ln::kThreads - 1) / ln::kThreads), ln::kSplits);
-    if (dtype == PARARNN_F32) {
-        ln::dx_kernel<float><<<grid, ln::kThreads, 0, st>>>(pr);
-        if (dL_dweight || dL_dbias) ln::columns_kernel<float><<<cols, ln::kThreads, 0, st>>>(pr);
-    } else {
-        ln::dx_kernel<ln::bf16><<<grid, ln::kThreads, 0, st>>>(pr);
-        if (dL_dweight || dL_dbias) ln::columns_kernel<ln::bf16><<<cols, ln::kThreads, 0, st>>>(pr);
-    }
-    s = abi::launched(who);
-    if (s != PARARNN_OK || !(dL_dweight || dL_dbias)) return s;
-    ln::reduce_kernel<<<(unsigned)((C + 127) / 128), 128, 0, st>>>(pr.part, dL_dweight, dL_dbias, C);
-    return abi::launched(who);
+    return dtype == PARARNN_F32 ? ln::launch_backward<float>(who, pr, dL_dweight, dL_dbias, st)
+                                : ln::launch_backward<ln::bf16>(who, pr, dL_dweight, dL_dbias, st);
 }
 
 }  // extern "C"

@@ -52,9 +52,13 @@ struct BwdParams {
 // A row of N values belongs to `tpr` threads (a power of two), each with K vectors of V
 // values, read and written once.  A thread's rows all have the same p, so that it
 // keeps its weights, and in the backward pass its column sums, in registers over all
-// its rows; the next row is read while the present one is reduced.  Bound by
-// HBM; two reductions of a row in the forward pass (the variance is taken about the
-// mean), one of two sums in the backward pass.
+// its rows.  U rows are read and reduced at a time: that keeps enough bytes in flight and
+// shares a block barrier between them.  Bound by HBM; two reductions of a row in
+// the forward pass (the variance is taken about the mean), one of two sums in the
+// backward pass.
+template <typename T, int V, int K>
+constexpr int words_of = K * (V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1);
+constexpr int batch_of(int words) { return words >= 16 ? 1 : words >= 8 ? 2 : 4; }
 template <typename T, int V>
 struct Vec {
     static constexpr int kWords = V * sizeof(T) / 4;
@@ -101,29 +105,33 @@ __device__ __forceinline__ void store(T* p, const float* v) {
     }
 }
 
-// The sum of two values over a row's threads.  Rows of more than a warp meet in shared
+// Sums over a row's threads of n values.  Rows of more than a warp meet in shared
 // memory, two buffers in turn; every thread of the block takes part.
-__device__ __forceinline__ float2 row_sum(float a, float b, int tpr, float2 (*buf)[32], int& turn) {
-    for (int o = min(tpr, 32) >> 1; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+template <int n>
+__device__ __forceinline__ void row_sums(float (&a)[n], int tpr, float (*buf)[32][n], int& turn) {
+    for (int o = min(tpr, 32) >> 1; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
     if (tpr > 32) {
         const int warp = threadIdx.x >> 5, per = tpr >> 5;
-        if ((threadIdx.x & 31) == 0) buf[turn][warp] = make_float2(a, b);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < n; ++i) buf[turn][warp][i] = a[i];
         __syncthreads();
-        const float2* q = buf[turn] + warp / per * per;
-        a = b = 0.0f;
-        for (int i = 0; i < per; ++i) a += q[i].x, b += q[i].y;
+        const float(*q)[n] = buf[turn] + warp / per * per;
+#pragma unroll
+        for (int i = 0; i < n; ++i) a[i] = 0.0f;
+        for (int w = 0; w < per; ++w)
+#pragma unroll
+            for (int i = 0; i < n; ++i) a[i] += q[w][i];
         turn ^= 1;
     }
-    return make_float2(a, b);
 }
 
 // the rows of this thread's group: m0, m0 + dm, ... below M with parameter row p
 struct Rows {
     int64_t p, m0, dm;
-    int64_t turns;  // of the whole block
+    int64_t steps;  // of the whole block: the most rows that one of its groups has
     bool on;
 };
 template <class P>
@@ -135,182 +143,247 @@ __device__ __forceinline__ Rows rows_of(const P& pr) {
     r.m0 = slot * pr.gpp + g / pr.pb;
     r.dm = slots * pr.gpp;
     r.on = g < pr.pb * pr.gpp && r.p < pr.P;
-    r.turns = (pr.M - slot * pr.gpp + r.dm - 1) / r.dm;
+    r.steps = (pr.M - slot * pr.gpp + r.dm - 1) / r.dm;
     return r;
 }
 
-template <typename T, int V, int K, bool kBig>
-__global__ void __launch_bounds__(kBig ? 1024 : 256) forward_rows(const Params pr) {
-    __shared__ float2 buf[2][32];
+// The E = K V values of a thread in pairs, so that two go through one packed instruction:
+// pair e is values 2e, 2e + 1.  Only where V is 1 can a pair be half inside the row.
+template <typename T, int V, int K>
+__device__ __forceinline__ f2 pair(const Vec<T, V> (&v)[K], int e) {
+    if constexpr (V == 1) return f2{value<T, V>(v[2 * e], 0), value<T, V>(v[2 * e + 1], 0)};
+    return f2{value<T, V>(v[2 * e / V], 2 * e % V), value<T, V>(v[2 * e / V], 2 * e % V + 1)};
+}
+// columns of a thread: which of its values lie in the row
+template <int V, int K>
+struct Columns {
+    int j0, dj, N;
+    __device__ __forceinline__ int of(int e) const { return j0 + e / V * dj + e % V; }
+    __device__ __forceinline__ bool in(int k) const { return j0 + k * dj < N; }
+    // a pair with zeros in place of the values past the row
+    __device__ __forceinline__ f2 mask(f2 x, int e) const {
+        const bool a = of(2 * e) < N, b = V == 1 ? of(2 * e + 1) < N : a;
+        return f2{a ? x.x : 0.0f, b ? x.y : 0.0f};
+    }
+};
+__device__ __forceinline__ float total(f2 x) { return x.x + x.y; }
+
+template <typename T, int V, int K, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_rows(const Params pr) {
+    constexpr int U = batch_of(words_of<T, V, K>), E = K * V;
+    constexpr bool kHold = E <= 16;  // weights in registers
+    __shared__ float buf[2][32][U];
     const Rows rows = rows_of(pr);
-    const int j0 = (threadIdx.x % pr.tpr) * V, dj = pr.tpr * V, N = (int)pr.N;
+    const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
+    const int N = c.N;
     const float inv = 1.0f / (float)N;
     int turn = 0;
-    float w[K * V], b[K * V], chk = 0.0f;
-    Vec<T, V> v[K], next[K];
-    const T* x = static_cast<const T*>(pr.x);
-    auto fetch = [&](int64_t m, Vec<T, V>* to) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            to[k] = Vec<T, V>{};
-            if (rows.on && m < pr.M && j0 + k * dj < N) to[k] = load<T, V>(x + (m * pr.P + rows.p) * N + j0 + k * dj);
-        }
-    };
-    auto params = [&]() {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int j = j0 + k * dj + i;
-                const bool in = rows.on && j < N;
-                w[k * V + i] = in && pr.w ? pr.w[rows.p * N + j] : 1.0f;
-                b[k * V + i] = in && pr.b ? pr.b[rows.p * N + j] : 0.0f;
+    f2 chk{0.0f, 0.0f}, w[kHold ? E / 2 : 1], b[kHold ? E / 2 : 1];
+    auto weight = [&](const float* from, int e, float none) {
+        f2 o{none, none};
+        if (from) {
+            if constexpr (V == 1) {
+                if (c.of(2 * e) < N) o.x = from[rows.p * N + c.of(2 * e)];
+                if (c.of(2 * e + 1) < N) o.y = from[rows.p * N + c.of(2 * e + 1)];
+            } else if (c.of(2 * e) < N) {
+                const float* q = from + rows.p * N + c.of(2 * e);
+                o = f2{q[0], q[1]};
             }
-    };
-    fetch(rows.m0, v);
-    if (!kBig) params();
-    for (int64_t it = 0; it < rows.turns; ++it) {
-        const int64_t m = rows.m0 + it * rows.dm;
-        if (!kBig) fetch(m + rows.dm, next);
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s += value<T, V>(v[k], i);
-        const float mean = row_sum(s, 0.0f, pr.tpr, buf, turn).x * inv;
-        s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (j0 + k * dj < N)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float c = value<T, V>(v[k], i) - mean;
-                    s = __fmaf_rn(c, c, s);
-                }
-        const float rstd = 1.0f / sqrtf(row_sum(s, 0.0f, pr.tpr, buf, turn).x * inv + pr.eps);
-        if (rows.on && m < pr.M) {
-            const int64_t row = m * pr.P + rows.p;
-            if (kBig) params();
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (j0 + k * dj < N) {
-                    float o[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        o[i] = __fmaf_rn((value<T, V>(v[k], i) - mean) * rstd, w[k * V + i], b[k * V + i]);
-                        chk = __fmaf_rn(o[i], 0.0f, chk);
-                    }
-                    store<T, V>(static_cast<T*>(pr.y) + row * N + j0 + k * dj, o);
-                }
-            if (j0 == 0 && pr.mean) pr.mean[row] = mean;
-            if (j0 == 0 && pr.rstd) pr.rstd[row] = rstd;
         }
-        if (kBig) {
-            fetch(m + rows.dm, v);
-        } else {
+        return o;
+    };
+    if (kHold && rows.on)
 #pragma unroll
-            for (int k = 0; k < K; ++k) v[k] = next[k];
+        for (int e = 0; e < E / 2; ++e) w[e] = weight(pr.w, e, 1.0f), b[e] = weight(pr.b, e, 0.0f);
+    for (int64_t it = 0; it < rows.steps; it += U) {
+        Vec<T, V> v[U][K];
+        float s[U], mean[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = rows.m0 + (it + u) * rows.dm;
+            const T* x = static_cast<const T*>(pr.x) + (m * pr.P + rows.p) * N + c.j0;
+            const bool on = rows.on && m < pr.M;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                v[u][k] = Vec<T, V>{};
+                if (on && c.in(k)) v[u][k] = load<T, V>(x + k * c.dj);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            f2 t{0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) t = add2(t, pair(v[u], e));
+            s[u] = total(t);
+        }
+        row_sums(s, pr.tpr, buf, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] = s[u] * inv;
+            f2 t{0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                const f2 d = c.mask(sub2(pair(v[u], e), splat2(mean[u])), e);
+                t = fma2(d, d, t);
+            }
+            s[u] = total(t);
+        }
+        row_sums(s, pr.tpr, buf, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = rows.m0 + (it + u) * rows.dm;
+            if (!rows.on || m >= pr.M) continue;
+            const float rstd = 1.0f / sqrtf(s[u] * inv + pr.eps);
+            const int64_t row = m * pr.P + rows.p;
+            T* y = static_cast<T*>(pr.y) + row * N + c.j0;
+            auto out = [&](int e) {
+                const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd));
+                f2 o;
+                if constexpr (kHold)
+                    o = fma2(xh, w[e], b[e]);
+                else
+                    o = fma2(xh, weight(pr.w, e, 1.0f), weight(pr.b, e, 0.0f));
+                chk = fma2(c.mask(o, e), splat2(0.0f), chk);
+                return o;
+            };
+            if constexpr (V == 1) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const f2 o = out(e);
+                    if (c.in(2 * e)) store<T, 1>(y + 2 * e * c.dj, &o.x);
+                    if (c.in(2 * e + 1)) store<T, 1>(y + (2 * e + 1) * c.dj, &o.y);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (c.in(k)) {
+                        float o[V];
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const f2 q = out(k * (V / 2) + i);
+                            o[2 * i] = q.x, o[2 * i + 1] = q.y;
+                        }
+                        store<T, V>(y + k * c.dj, o);
+                    }
+            }
+            if (c.j0 == 0 && pr.mean) pr.mean[row] = mean[u];
+            if (c.j0 == 0 && pr.rstd) pr.rstd[row] = rstd;
         }
     }
-    if (chk != chk && pr.status) atomicOr(pr.status, kStatusNonFinite);
+    if (pr.status && total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
 }
 
-template <typename T, int V, int K, bool kBig>
-__global__ void __launch_bounds__(kBig ? 1024 : 256) backward_rows(const BwdParams pr) {
-    __shared__ float2 buf[2][32];
+template <typename T, int V, int K, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_rows(const BwdParams pr) {
+    constexpr int U = kThreads > 512 ? 1 : batch_of(words_of<T, V, K>), E = K * V;
+    constexpr bool kHold = kThreads <= 512;
+    __shared__ float buf[2][32][2 * U];
     extern __shared__ float2 sums[];  // [K * V][threads]
     const Rows rows = rows_of(pr);
-    const int j0 = (threadIdx.x % pr.tpr) * V, dj = pr.tpr * V, N = (int)pr.N;
+    const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
+    const int N = c.N;
     const float inv = 1.0f / (float)N;
     int turn = 0;
-    float w[K * V], dw[K * V], db[K * V], chk = 0.0f;
-    Vec<T, V> v[K], g[K], nv[K], ng[K];
-    float mean = 0.0f, rstd = 0.0f, nmean = 0.0f, nrstd = 0.0f;
-    auto fetch = [&](int64_t m, Vec<T, V>* x, Vec<T, V>* dy, float& mu, float& rs) {
-        const bool on = rows.on && m < pr.M;
-        const int64_t row = on ? m * pr.P + rows.p : 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            x[k] = Vec<T, V>{};
-            dy[k] = Vec<T, V>{};
-            if (on && j0 + k * dj < N) {
-                x[k] = load<T, V>(static_cast<const T*>(pr.x) + row * N + j0 + k * dj);
-                dy[k] = load<T, V>(static_cast<const T*>(pr.dy) + row * N + j0 + k * dj);
-            }
-        }
-        mu = on ? pr.mean[row] : 0.0f;
-        rs = on ? pr.rstd[row] : 0.0f;
-    };
+    f2 w[E / 2], dw[E / 2], db[E / 2], chk{0.0f, 0.0f};
     auto params = [&]() {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int j = j0 + k * dj + i;
-                w[k * V + i] = rows.on && j < N && pr.w ? pr.w[rows.p * N + j] : 1.0f;
+        for (int e = 0; e < E / 2; ++e) {
+            w[e] = splat2(1.0f);
+            if (pr.w && rows.on) {
+                if (c.of(2 * e) < N) w[e].x = pr.w[rows.p * N + c.of(2 * e)];
+                if (c.of(2 * e + 1) < N) w[e].y = pr.w[rows.p * N + c.of(2 * e + 1)];
             }
+        }
     };
 #pragma unroll
-    for (int e = 0; e < K * V; ++e) dw[e] = db[e] = 0.0f;
-    fetch(rows.m0, v, g, mean, rstd);
-    if (!kBig) params();
-    for (int64_t it = 0; it < rows.turns; ++it) {
-        const int64_t m = rows.m0 + it * rows.dm;
-        if (!kBig) fetch(m + rows.dm, nv, ng, nmean, nrstd);
-        if (kBig) params();
-        float s1 = 0.0f, s2 = 0.0f;
-        // the threads past N and the rows past M hold zeros: they add nothing but -mean * 0
+    for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = splat2(0.0f);
+    if (kHold) params();
+    for (int64_t it = 0; it < rows.steps; it += U) {
+        Vec<T, V> v[U][K], g[U][K];
+        float mean[U], rstd[U], s[2 * U];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = rows.m0 + (it + u) * rows.dm;
+            const bool on = rows.on && m < pr.M;
+            const int64_t row = on ? m * pr.P + rows.p : 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float dy = value<T, V>(g[k], i), xh = (value<T, V>(v[k], i) - mean) * rstd;
-                const float d = dy * w[k * V + i];
-                s1 += d;
-                s2 = __fmaf_rn(d, xh, s2);
-                if (j0 + k * dj < N) {
-                    db[k * V + i] += dy;
-                    dw[k * V + i] = __fmaf_rn(dy, xh, dw[k * V + i]);
+            for (int k = 0; k < K; ++k) {
+                v[u][k] = Vec<T, V>{};
+                g[u][k] = Vec<T, V>{};
+                if (on && c.in(k)) {
+                    v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + row * N + c.j0 + k * c.dj);
+                    g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + row * N + c.j0 + k * c.dj);
                 }
             }
-        const float2 t = row_sum(s1, s2, pr.tpr, buf, turn);
-        const float m1 = t.x * inv, m2 = t.y * inv;
-        if (rows.on && m < pr.M) {
-            T* o = static_cast<T*>(pr.dx) + (m * pr.P + rows.p) * N + j0;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (j0 + k * dj < N) {
-                    float q[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = (value<T, V>(v[k], i) - mean) * rstd;
-                        q[i] = rstd * (__fmaf_rn(value<T, V>(g[k], i), w[k * V + i], -m1) - xh * m2);
-                        chk = __fmaf_rn(q[i], 0.0f, chk);
-                    }
-                    store<T, V>(o + k * dj, q);
-                }
+            mean[u] = on ? pr.mean[row] : 0.0f;
+            rstd[u] = on ? pr.rstd[row] : 0.0f;
         }
-        if (kBig) {
-            fetch(m + rows.dm, v, g, mean, rstd);
-        } else {
+        if (!kHold) params();
+        // rows past M hold zeros: they add nothing
 #pragma unroll
-            for (int k = 0; k < K; ++k) v[k] = nv[k], g[k] = ng[k];
-            mean = nmean;
-            rstd = nrstd;
+        for (int u = 0; u < U; ++u) {
+            f2 t1{0.0f, 0.0f}, t2 = t1;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                // past the row dy is zero, but the mean need not be finite
+                const f2 xh = c.mask(mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u])), e);
+                const f2 dy = pair(g[u], e), d = mul2(dy, w[e]);
+                t1 = add2(t1, d);
+                t2 = fma2(d, xh, t2);
+                db[e] = add2(db[e], dy);
+                dw[e] = fma2(dy, xh, dw[e]);
+            }
+            s[2 * u] = total(t1);
+            s[2 * u + 1] = total(t2);
+        }
+        row_sums(s, pr.tpr, buf, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = rows.m0 + (it + u) * rows.dm;
+            if (!rows.on || m >= pr.M) continue;
+            const f2 m1 = splat2(s[2 * u] * inv), m2 = splat2(-s[2 * u + 1] * inv);
+            T* o = static_cast<T*>(pr.dx) + (m * pr.P + rows.p) * N + c.j0;
+            auto out = [&](int e) {
+                const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u]));
+                const f2 q = mul2(fma2(xh, m2, sub2(mul2(pair(g[u], e), w[e]), m1)), splat2(rstd[u]));
+                chk = fma2(c.mask(q, e), splat2(0.0f), chk);
+                return q;
+            };
+            if constexpr (V == 1) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const f2 q = out(e);
+                    if (c.in(2 * e)) store<T, 1>(o + 2 * e * c.dj, &q.x);
+                    if (c.in(2 * e + 1)) store<T, 1>(o + (2 * e + 1) * c.dj, &q.y);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (c.in(k)) {
+                        float q[V];
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const f2 t = out(k * (V / 2) + i);
+                            q[2 * i] = t.x, q[2 * i + 1] = t.y;
+                        }
+                        store<T, V>(o + k * c.dj, q);
+                    }
+            }
         }
     }
-    if (chk != chk) atomicOr(pr.status, kStatusNonFinite);
+    if (total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
     if (!pr.part) return;
     // the block's column sums: the groups of one parameter row in order
 #pragma unroll
-    for (int e = 0; e < K * V; ++e) sums[e * blockDim.x + threadIdx.x] = make_float2(dw[e], db[e]);
+    for (int e = 0; e < E; ++e)
+        sums[e * blockDim.x + threadIdx.x] = e & 1 ? make_float2(dw[e / 2].y, db[e / 2].y) : make_float2(dw[e / 2].x, db[e / 2].x);
     __syncthreads();
     const int g0 = threadIdx.x / pr.tpr;
     if (g0 < pr.pb && rows.p < pr.P) {
         float* to = pr.part + (int64_t)(blockIdx.x / pr.npc) * 2 * pr.P * N + rows.p * N;
 #pragma unroll
-        for (int e = 0; e < K * V; ++e) {
-            const int j = j0 + e / V * dj + e % V;
+        for (int e = 0; e < E; ++e) {
+            const int j = c.of(e);
             float2 t = make_float2(0.0f, 0.0f);
             for (int q = 0; q < pr.gpp; ++q) {
                 const float2 u = sums[e * blockDim.x + threadIdx.x + q * pr.pb * pr.tpr];
@@ -456,7 +529,7 @@ namespace {
 
 struct Plan {
     int vec, each;  // values per access and per thread; 0: rows of any length
-    bool big;
+    int most;  // threads that the kernel is compiled for
     int tpr, threads, pb, gpp, npc;
 };
 
@@ -466,16 +539,21 @@ int pow2_at_least(int64_t n) {
     return p;
 }
 
-// Values per thread: 8 as long as 256 threads hold the row, then 16, and past
-// 256 threads' registers blocks of up to 1024 threads that read the weights with each row.
-Plan plan_of(int64_t P, int64_t N, int esz, bool by16, bool by4) {
+// Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
+// of float32, so that short and middle rows need no block barrier; the backward
+// pass, which holds two column sums for each value, has 8, or 16 past 2048 columns.
+Plan plan_of(int64_t P, int64_t N, int esz, bool by16, bool by4, bool forward) {
     Plan p{};
     p.vec = by16 ? 16 / esz : (esz == 2 && by4) ? 2 : 1;
     if (N > 16384) return Plan{};
-    p.big = N > 4096;
-    p.each = N > 2048 ? 16 : 8;
+    const int most = forward && by16 ? 128 / esz : 16;
+    p.each = 8;
+    if (forward && by16)
+        while (p.each < most && p.each * 32 < N) p.each *= 2;
+    else if (N > 2048)
+        p.each = 16;
     p.tpr = pow2_at_least((N + p.each - 1) / p.each);
-    p.threads = p.big ? p.tpr : 256;
+    p.threads = p.most = std::max(p.tpr, 256);
     const int groups = p.threads / p.tpr;
     p.pb = (int)std::min<int64_t>(P, groups);
     p.gpp = groups / p.pb;
@@ -483,25 +561,33 @@ Plan plan_of(int64_t P, int64_t N, int esz, bool by16, bool by4) {
     return p;
 }
 
-// calls f with the values per access, the accesses per thread and `big` as types
-template <typename T, class F>
-bool with_shape(const Plan& p, F f) {
-#define PARARNN_LN(V, E, B)                                                                                       \
-    if (p.vec == V && p.each == E && p.big == B) {                                                                \
-        f(std::integral_constant<int, V>{}, std::integral_constant<int, E / V>{}, std::integral_constant<bool, B>{}); \
-        return true;                                                                                              \
-    }
-#define PARARNN_LN_ALL(V) PARARNN_LN(V, 8, false) PARARNN_LN(V, 16, false) PARARNN_LN(V, 16, true)
-    if constexpr (sizeof(T) == 2) {
-        PARARNN_LN_ALL(8)
-        PARARNN_LN_ALL(2)
+// calls f with the values per access, the accesses per thread and the threads as types
+template <typename T, bool kForward, class F>
+void with_shape(const Plan& p, F f) {
+#define PARARNN_LN(V, E, B) \
+    if (p.vec == V && p.each == E && p.most == B)  \
+        return f(std::integral_constant<int, V>{}, std::integral_constant<int, E / V>{}, std::integral_constant<int, B>{});
+#define PARARNN_LN_ALL(V) \
+    PARARNN_LN(V, 8, 256) PARARNN_LN(V, 16, 256) PARARNN_LN(V, 16, 512) PARARNN_LN(V, 16, 1024)
+    constexpr int full = 16 / sizeof(T);
+    if constexpr (kForward) {
+        PARARNN_LN(full, 8, 256)
+        PARARNN_LN(full, 16, 256)
+        PARARNN_LN(full, 32, 256)
+        if constexpr (sizeof(T) == 2) {
+            PARARNN_LN(full, 64, 256)
+        } else {
+            PARARNN_LN(full, 32, 512)
+        }
     } else {
-        PARARNN_LN_ALL(4)
+        PARARNN_LN_ALL(full)
+    }
+    if constexpr (sizeof(T) == 2) {
+        PARARNN_LN_ALL(2)
     }
     PARARNN_LN_ALL(1)
 #undef PARARNN_LN_ALL
 #undef PARARNN_LN
-    return false;
 }
 
 int sm_count() {
@@ -528,14 +614,14 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
     const bool by16 = (pr.N * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.x, 16) && !abi::misaligned(pr.y, 16);
     const bool by4 = (pr.N * sizeof(T)) % 4 == 0 && !abi::misaligned(pr.x, 4) && !abi::misaligned(pr.y, 4);
-    const Plan p = plan_of(pr.P, pr.N, sizeof(T), by16, by4);
+    const Plan p = plan_of(pr.P, pr.N, sizeof(T), by16, by4, true);
     if (!p.vec) {
         forward_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
         return abi::launched(who);
     }
     pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
-    const int64_t blocks = slots_for(p, pr.M, sms, p.big ? 1024 : p.each == 16 ? 768 : 1024) * p.npc;
-    with_shape<T>(p, [&](auto v, auto k, auto big) {
+    const int64_t blocks = slots_for(p, pr.M, sms, p.most == 256 ? 768 : p.most) * p.npc;
+    with_shape<T, true>(p, [&](auto v, auto k, auto big) {
         forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>
             <<<(unsigned)blocks, p.threads, 0, st>>>(pr);
     });
@@ -552,7 +638,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
         return (pr.N * sizeof(T)) % a == 0 && !abi::misaligned(pr.x, a) && !abi::misaligned(pr.dy, a) &&
                !abi::misaligned(pr.dx, a);
     };
-    const Plan p = plan_of(pr.P, pr.N, sizeof(T), ok(16), ok(4));
+    const Plan p = plan_of(pr.P, pr.N, sizeof(T), ok(16), ok(4), false);
     if (!sums) pr.part = nullptr;
     int64_t parts;
     if (!p.vec) {
@@ -562,9 +648,9 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
         dx_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
     } else {
         pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
-        parts = slots_for(p, pr.M, sms, p.big ? 1024 : 512);
+        parts = slots_for(p, pr.M, sms, p.most == 256 ? 512 : p.most);
         if (sums) parts = std::min<int64_t>(parts, max_parts(pr.M, C));
-        with_shape<T>(p, [&](auto v, auto k, auto big) {
+        with_shape<T, false>(p, [&](auto v, auto k, auto big) {
             constexpr int each = decltype(v)::value * decltype(k)::value;
             auto kern = backward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
             const size_t smem = sums ? (size_t)each * p.threads * sizeof(float2) : 0;

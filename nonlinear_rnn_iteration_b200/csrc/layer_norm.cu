@@ -160,10 +160,24 @@ struct Columns {
     int j0, dj, N;
     __device__ __forceinline__ int of(int e) const { return j0 + e / V * dj + e % V; }
     __device__ __forceinline__ bool in(int k) const { return j0 + k * dj < N; }
-    // a pair with zeros in place of the values past the row
+    // a pair with zeros in place of the values past the row, where V is 1
     __device__ __forceinline__ f2 mask(f2 x, int e) const {
-        const bool a = of(2 * e) < N, b = V == 1 ? of(2 * e + 1) < N : a;
-        return f2{a ? x.x : 0.0f, b ? x.y : 0.0f};
+        if constexpr (V > 1) return x;
+        return f2{in(2 * e) ? x.x : 0.0f, in(2 * e + 1) ? x.y : 0.0f};
+    }
+    // f(e) for the pairs that lie in the row, at least in part
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int e = 0; e < K / 2; ++e) f(e);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in(k))
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) f(k * (V / 2) + i);
+        }
     }
 };
 __device__ __forceinline__ float total(f2 x) { return x.x + x.y; }
@@ -171,8 +185,10 @@ __device__ __forceinline__ float total(f2 x) { return x.x + x.y; }
 template <typename T, int V, int K, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_rows(const Params pr) {
     constexpr int U = batch_of(words_of<T, V, K>), E = K * V;
-    constexpr bool kHold = E <= 16;  // weights in registers
+    // the weights in registers, or, for more values, in shared memory: [w, b][quads][threads of a row]
+    constexpr bool kHold = E <= 16;
     __shared__ float buf[2][32][U];
+    extern __shared__ float4 held[];
     const Rows rows = rows_of(pr);
     const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c.N;
@@ -192,9 +208,23 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         }
         return o;
     };
-    if (kHold && rows.on)
+    const int quads = pr.tpr * (E / 4), at = c.j0 / V;
+    if constexpr (kHold) {
+        if (rows.on)
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w[e] = weight(pr.w, e, 1.0f), b[e] = weight(pr.b, e, 0.0f);
+            for (int e = 0; e < E / 2; ++e) w[e] = weight(pr.w, e, 1.0f), b[e] = weight(pr.b, e, 0.0f);
+    } else {
+        // the block's rows share one parameter row; its first group lays it out
+        if ((int)threadIdx.x < pr.tpr)
+#pragma unroll
+            for (int e = 0; e < E / 2; e += 2) {
+                f2 q = weight(pr.w, e, 1.0f), r = weight(pr.w, e + 1, 1.0f);
+                held[e / 2 * pr.tpr + at] = make_float4(q.x, q.y, r.x, r.y);
+                q = weight(pr.b, e, 0.0f), r = weight(pr.b, e + 1, 0.0f);
+                held[quads + e / 2 * pr.tpr + at] = make_float4(q.x, q.y, r.x, r.y);
+            }
+        __syncthreads();
+    }
     for (int64_t it = 0; it < rows.steps; it += U) {
         Vec<T, V> v[U][K];
         float s[U], mean[U];
@@ -221,11 +251,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         for (int u = 0; u < U; ++u) {
             mean[u] = s[u] * inv;
             f2 t{0.0f, 0.0f};
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
+            c.each([&](int e) {
                 const f2 d = c.mask(sub2(pair(v[u], e), splat2(mean[u])), e);
                 t = fma2(d, d, t);
-            }
+            });
             s[u] = total(t);
         }
         row_sums(s, pr.tpr, buf, turn);
@@ -236,20 +265,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
             const float rstd = 1.0f / sqrtf(s[u] * inv + pr.eps);
             const int64_t row = m * pr.P + rows.p;
             T* y = static_cast<T*>(pr.y) + row * N + c.j0;
-            auto out = [&](int e) {
+            auto out = [&](int e, f2 we, f2 be) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd));
-                f2 o;
-                if constexpr (kHold)
-                    o = fma2(xh, w[e], b[e]);
-                else
-                    o = fma2(xh, weight(pr.w, e, 1.0f), weight(pr.b, e, 0.0f));
+                const f2 o = fma2(xh, we, be);
                 chk = fma2(c.mask(o, e), splat2(0.0f), chk);
                 return o;
             };
             if constexpr (V == 1) {
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
-                    const f2 o = out(e);
+                    const f2 o = out(e, w[e], b[e]);
                     if (c.in(2 * e)) store<T, 1>(y + 2 * e * c.dj, &o.x);
                     if (c.in(2 * e + 1)) store<T, 1>(y + (2 * e + 1) * c.dj, &o.y);
                 }
@@ -260,7 +285,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                         float o[V];
 #pragma unroll
                         for (int i = 0; i < V / 2; ++i) {
-                            const f2 q = out(k * (V / 2) + i);
+                            const int e = k * (V / 2) + i;
+                            f2 we, be;
+                            if constexpr (kHold) {
+                                we = w[e], be = b[e];
+                            } else {
+                                const float4 q = held[e / 2 * pr.tpr + at], r = held[quads + e / 2 * pr.tpr + at];
+                                we = e & 1 ? f2{q.z, q.w} : f2{q.x, q.y};
+                                be = e & 1 ? f2{r.z, r.w} : f2{r.x, r.y};
+                            }
+                            const f2 q = out(e, we, be);
                             o[2 * i] = q.x, o[2 * i + 1] = q.y;
                         }
                         store<T, V>(y + k * c.dj, o);
@@ -323,8 +357,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             f2 t1{0.0f, 0.0f}, t2 = t1;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
+            c.each([&](int e) {
                 // past the row dy is zero, but the mean need not be finite
                 const f2 xh = c.mask(mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u])), e);
                 const f2 dy = pair(g[u], e), d = mul2(dy, w[e]);
@@ -332,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                 t2 = fma2(d, xh, t2);
                 db[e] = add2(db[e], dy);
                 dw[e] = fma2(dy, xh, dw[e]);
-            }
+            });
             s[2 * u] = total(t1);
             s[2 * u + 1] = total(t2);
         }
@@ -542,20 +575,24 @@ int pow2_at_least(int64_t n) {
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
 // of float32, so that short and middle rows need no block barrier; the backward
 // pass, which holds two column sums for each value, has 8, or 16 past 2048 columns.
-Plan plan_of(int64_t P, int64_t N, int esz, bool by16, bool by4, bool forward) {
+// With few rows the smaller count leaves more threads to each of them.  A row of 256 bytes or
+// more needs no neighbours: the block's rows then share one parameter row.
+Plan plan_of(int64_t M, int64_t P, int64_t N, int esz, bool by16, bool by4, bool forward, int sms) {
     Plan p{};
     p.vec = by16 ? 16 / esz : (esz == 2 && by4) ? 2 : 1;
     if (N > 16384) return Plan{};
     const int most = forward && by16 ? 128 / esz : 16;
     p.each = 8;
     if (forward && by16)
-        while (p.each < most && p.each * 32 < N) p.each *= 2;
+        while (p.each < most && p.each * 32 < N && (double)M * P * N >= 768.0 * sms * p.each) p.each *= 2;
+    if (forward && by16)
+        while (p.each < most && p.each * 1024 < N) p.each *= 2;
     else if (N > 2048)
         p.each = 16;
     p.tpr = pow2_at_least((N + p.each - 1) / p.each);
     p.threads = p.most = std::max(p.tpr, 256);
     const int groups = p.threads / p.tpr;
-    p.pb = (int)std::min<int64_t>(P, groups);
+    p.pb = N * esz >= 256 ? 1 : (int)std::min<int64_t>(P, groups);
     p.gpp = groups / p.pb;
     p.npc = (int)((P + p.pb - 1) / p.pb);
     return p;
@@ -571,13 +608,13 @@ void with_shape(const Plan& p, F f) {
     PARARNN_LN(V, 8, 256) PARARNN_LN(V, 16, 256) PARARNN_LN(V, 16, 512) PARARNN_LN(V, 16, 1024)
     constexpr int full = 16 / sizeof(T);
     if constexpr (kForward) {
-        PARARNN_LN(full, 8, 256)
-        PARARNN_LN(full, 16, 256)
+        PARARNN_LN_ALL(full)
+        PARARNN_LN(full, 8, 512)
+        PARARNN_LN(full, 8, 1024)
         PARARNN_LN(full, 32, 256)
+        PARARNN_LN(full, 32, 512)
         if constexpr (sizeof(T) == 2) {
             PARARNN_LN(full, 64, 256)
-        } else {
-            PARARNN_LN(full, 32, 512)
         }
     } else {
         PARARNN_LN_ALL(full)
@@ -614,7 +651,7 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
     const bool by16 = (pr.N * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.x, 16) && !abi::misaligned(pr.y, 16);
     const bool by4 = (pr.N * sizeof(T)) % 4 == 0 && !abi::misaligned(pr.x, 4) && !abi::misaligned(pr.y, 4);
-    const Plan p = plan_of(pr.P, pr.N, sizeof(T), by16, by4, true);
+    const Plan p = plan_of(pr.M, pr.P, pr.N, sizeof(T), by16, by4, true, sms);
     if (!p.vec) {
         forward_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
         return abi::launched(who);
@@ -622,8 +659,10 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
     const int64_t blocks = slots_for(p, pr.M, sms, p.most == 256 ? 768 : p.most) * p.npc;
     with_shape<T, true>(p, [&](auto v, auto k, auto big) {
-        forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>
-            <<<(unsigned)blocks, p.threads, 0, st>>>(pr);
+        auto kern = forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
+        const size_t smem = p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0;
+        if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        kern<<<(unsigned)blocks, p.threads, smem, st>>>(pr);
     });
     return abi::launched(who);
 }
@@ -638,7 +677,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
         return (pr.N * sizeof(T)) % a == 0 && !abi::misaligned(pr.x, a) && !abi::misaligned(pr.dy, a) &&
                !abi::misaligned(pr.dx, a);
     };
-    const Plan p = plan_of(pr.P, pr.N, sizeof(T), ok(16), ok(4), false);
+    const Plan p = plan_of(pr.M, pr.P, pr.N, sizeof(T), ok(16), ok(4), false, sms);
     if (!sums) pr.part = nullptr;
     int64_t parts;
     if (!p.vec) {
@@ -654,7 +693,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
             constexpr int each = decltype(v)::value * decltype(k)::value;
             auto kern = backward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
             const size_t smem = sums ? (size_t)each * p.threads * sizeof(float2) : 0;
-            if (smem > 48 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             kern<<<(unsigned)(parts * p.npc), p.threads, smem, st>>>(pr);
         });
     }

@@ -29,7 +29,6 @@ pararnn_status encode_steps_map(CUtensorMap* map, const void* base, bool bf16, i
 namespace gs {
 
 typedef __nv_bfloat16 bf16;
-constexpr int kThreads = 128;
 // steps between two states that the forward keeps for the adjoint: a warp's share of a tile
 constexpr int kCkSteps = 8;
 
@@ -814,27 +813,107 @@ struct StepParams {
     float decay;
 };
 
-// one thread per channel walks the rows in order
-template <typename T>
-__global__ void __launch_bounds__(kThreads) step_kernel(const StepParams pr) {
-    const int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (d >= pr.D) return;
-    const float k = pr.decay * softplus_f(pr.lam[d]);
-    unsigned bad = 0;
-    for (int64_t n = 0; n < pr.N; ++n) {
-        const int64_t slot = pr.slots ? pr.slots[n] : n;
-        if (slot < 0 || slot >= pr.n_slots) {
-            if (slot >= pr.n_slots) bad |= kStatusBadIndex;
-            continue;
-        }
-        const T* p = static_cast<const T*>(pr.px) + n * 3 * pr.D + d;
-        const Row g = gates(PxTraits<T>::cvt(p[0]), PxTraits<T>::cvt(p[pr.D]), PxTraits<T>::cvt(p[2 * pr.D]), k);
-        const float h = __fmaf_rn(g.a, pr.state[slot * pr.D + d], sqrtf(g.v) * g.i * g.x);
-        pr.state[slot * pr.D + d] = h;
-        static_cast<T*>(pr.y)[n * pr.D + d] = to_out<T>(h);
-        if (!isfinite(h)) bad |= kStatusNonFinite;
+// A block takes one row and 256 V channels; it is bound by the latency of its loads for
+// few rows and by HBM for many.  Rows that name the same slot must be taken in order:
+// the block of the first of them takes them all, each with the state that the one before left,
+// and the others' blocks end.  Every block looks through the slots for that, N
+// words that the L2 cache holds, while its own loads are on their way.
+constexpr int kStepThreads = 256;
+constexpr int kStepRows = 8192;  // rows of one launch
+
+template <typename T, int V>
+__device__ __forceinline__ void step_load(const T* p, float (&o)[V]) {
+    if constexpr (V == 4 && sizeof(T) == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    } else if constexpr (V == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        o[0] = __uint_as_float(v.x << 16), o[1] = __uint_as_float(v.x & 0xffff0000u);
+        o[2] = __uint_as_float(v.y << 16), o[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+        o[0] = PxTraits<T>::cvt(p[0]);
     }
-    if (bad && pr.status) atomicOr(pr.status, bad);
+}
+template <typename T, int V>
+__device__ __forceinline__ void step_store(T* p, const float (&v)[V]) {
+    if constexpr (V == 4 && sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (V == 4) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+        p[0] = to_out<T>(v[0]);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const StepParams pr) {
+    __shared__ unsigned more[kStepRows / 32];  // rows behind this one that name its slot
+    __shared__ unsigned found;                 // 1: a row before it names the slot, 2: one behind it
+    const int n0 = (int)blockIdx.x, N = (int)pr.N, tid = threadIdx.x;
+    const int64_t D = pr.D, d = ((int64_t)blockIdx.y * kStepThreads + tid) * V;
+    const bool in = d < D;
+    const int64_t slot = pr.slots ? pr.slots[n0] : n0;
+    if (slot < 0 || slot >= pr.n_slots) {
+        if (slot >= 0 && pr.status && tid == 0) atomicOr(pr.status, kStatusBadIndex);
+        return;
+    }
+    const T* px = static_cast<const T*>(pr.px) + (int64_t)n0 * 3 * D + d;
+    float* state = pr.state + slot * D + d;
+    float p[3][V], h[V], k[V];
+    if (in) {
+#pragma unroll
+        for (int g = 0; g < 3; ++g) step_load<T, V>(px + g * D, p[g]);
+        step_load<float, V>(state, h);
+        step_load<float, V>(pr.lam + d, k);
+    }
+    bool chain = false;
+    if (pr.slots) {
+        for (int i = tid; i < (N + 31) / 32; i += kStepThreads) more[i] = 0;
+        if (tid == 0) found = 0;
+        __syncthreads();
+        auto look = [&](int j, int32_t other) {
+            if (other == (int32_t)slot && j != n0) {
+                if (j > n0) atomicOr(&more[j >> 5], 1u << (j & 31));
+                atomicOr(&found, j < n0 ? 1u : 2u);
+            }
+        };
+        const int quads = (reinterpret_cast<uintptr_t>(pr.slots) & 15) == 0 ? N / 4 : 0;
+#pragma unroll 4
+        for (int j = tid; j < quads; j += kStepThreads) {
+            const int4 q = reinterpret_cast<const int4*>(pr.slots)[j];
+            look(4 * j, q.x);
+            look(4 * j + 1, q.y);
+            look(4 * j + 2, q.z);
+            look(4 * j + 3, q.w);
+        }
+        for (int j = 4 * quads + tid; j < N; j += kStepThreads) look(j, pr.slots[j]);
+        __syncthreads();
+        if (found & 1) return;
+        chain = found & 2;
+    }
+    if (!in) return;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) k[i] = pr.decay * softplus_f(k[i]);
+    for (int n = n0;;) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Row g = gates(p[0][i], p[1][i], p[2][i], k[i]);
+            h[i] = __fmaf_rn(g.a, h[i], sqrtf(g.v) * g.i * g.x);
+            bad |= !isfinite(h[i]);
+        }
+        step_store<T, V>(static_cast<T*>(pr.y) + (int64_t)n * D + d, h);
+        if (!chain) break;
+        do ++n;
+        while (n < N && !(more[n >> 5] >> (n & 31) & 1));
+        if (n == N) break;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) step_load<T, V>(static_cast<const T*>(pr.px) + ((int64_t)n * 3 + g) * D + d, p[g]);
+    }
+    step_store<float, V>(state, h);
+    if (bad && pr.status) atomicOr(pr.status, kStatusNonFinite);
 }
 
 bool bad_sizes(int64_t B, int64_t T, int64_t D) {
@@ -970,6 +1049,33 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
             who, pr, map, blocks, pr.ranks, smem, st);
     });
     return s;
+}
+
+template <typename T>
+pararnn_status launch_step(const char* who, StepParams pr, cudaStream_t st) {
+    const bool quads = pr.D % 4 == 0 && !abi::misaligned(pr.px, 4 * sizeof(T)) && !abi::misaligned(pr.y, 4 * sizeof(T)) &&
+                       !abi::misaligned(pr.lam, 16) && !abi::misaligned(pr.state, 16);
+    const int64_t per = kStepThreads * (quads ? 4 : 1), chunks = (pr.D + per - 1) / per;
+    if (chunks > 65535) return abi::fail(who, "too many channels");
+    const int64_t N = pr.N;
+    // rows of a later launch come after those of an earlier one, as the order of rows wants it
+    for (int64_t n = 0; n < N; n += kStepRows) {
+        pr.N = N - n < kStepRows ? N - n : kStepRows;
+        const dim3 grid((unsigned)pr.N, (unsigned)chunks);
+        if (quads)
+            step_kernel<T, 4><<<grid, kStepThreads, 0, st>>>(pr);
+        else
+            step_kernel<T, 1><<<grid, kStepThreads, 0, st>>>(pr);
+        const pararnn_status s = abi::launched(who);
+        if (s != PARARNN_OK) return s;
+        pr.px = static_cast<const T*>(pr.px) + kStepRows * 3 * pr.D;
+        pr.y = static_cast<T*>(pr.y) + kStepRows * pr.D;
+        if (pr.slots)
+            pr.slots += kStepRows;
+        else
+            pr.state += kStepRows * pr.D, pr.n_slots -= kStepRows;
+    }
+    return PARARNN_OK;
 }
 
 }  // namespace
@@ -1115,12 +1221,7 @@ pararnn_status pararnn_gated_scan_step(int64_t N, int64_t D, pararnn_dtype dtype
     pr.D = D;
     pr.n_slots = n_slots;
     pr.decay = decay;
-    const unsigned grid = (unsigned)((D + gs::kThreads - 1) / gs::kThreads);
-    if (dtype == PARARNN_F32)
-        gs::step_kernel<float><<<grid, gs::kThreads, 0, st>>>(pr);
-    else
-        gs::step_kernel<gs::bf16><<<grid, gs::kThreads, 0, st>>>(pr);
-    return abi::launched(who);
+    return dtype == PARARNN_F32 ? gs::launch_step<float>(who, pr, st) : gs::launch_step<gs::bf16>(who, pr, st);
 }
 
 }  // extern "C"

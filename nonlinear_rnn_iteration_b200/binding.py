@@ -499,69 +499,75 @@ def newton_step_host(cell, px_host, dL_dH_host, diag_w=None, h0=None, K=1, chann
 
 
 # ---- gated linear recurrence and layer normalisation ------------------------
+# These calls are short enough that a decoding loop is bound by the host: the
+# checks below read each tensor's attributes once.
 
 def _same_device(px, *tensors):
-    """Every given tensor is contiguous and on px's CUDA device."""
-    if px.device.type != "cuda":
+    """Every given tensor is contiguous and on px's CUDA device, whose index is returned."""
+    dev = px.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device, got %s" % px.device)
-    for t in (px,) + tensors:
-        if t is None:
-            continue
-        if t.device != px.device:
-            raise ValueError("tensors on different devices: %s and %s" % (px.device, t.device))
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous, got strides %s" % (t.stride(),))
+    if not px.is_contiguous():
+        raise ValueError("tensors must be contiguous, got strides %s" % (px.stride(),))
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError("tensors on different devices: %s and %s" % (px.device, t.device))
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous, got strides %s" % (t.stride(),))
+    return dev
 
 
 def _expect(name, t, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError("%s must be %s %s, got %s %s" % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
 
 
-def _launch(call, px, stream, scratch):
-    """Runs call(stream) with px's device current.  Memory in `scratch` was
-    allocated here on torch's current stream: when the call runs on another
-    stream, the allocator is told, so that it is not handed out again before
-    that stream is done with it."""
+def _launch(where, fn, dev, stream, scratch, workspace, sync_status, args):
+    """fn(*args, workspace, its bytes, stream) with device `dev` current, and its
+    status.  Memory in `scratch` was allocated here on torch's current stream:
+    when the call runs on another stream, the allocator is told, so that it is
+    not handed out again before that stream is done with it."""
     import torch
 
-    with torch.cuda.device(px.device):
-        cur = torch.cuda.current_stream(px.device)
-        st = stream if stream is not None else cur
-        handle = _stream(st)
-        if handle != cur.cuda_stream:
-            ext = st if not isinstance(st, int) else torch.cuda.ExternalStream(st, device=px.device)
-            ext.wait_stream(cur)  # the memory may still be in use by earlier work of the stream it came from
-            for t in scratch:
-                if t is not None:
-                    t.record_stream(ext)
-        return call(handle)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(where, fn, dev, stream, scratch, workspace, sync_status, args)
+    cur = torch.cuda.current_stream(dev)
+    handle = cur.cuda_stream if stream is None else (stream if isinstance(stream, int) else stream.cuda_stream)
+    if handle != cur.cuda_stream:
+        ext = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        ext.wait_stream(cur)  # the memory may still be in use by earlier work of the stream it came from
+        for t in scratch:
+            if t is not None:
+                t.record_stream(ext)
+    if workspace is None:
+        status = fn(*args, None, 0, handle)
+    else:
+        status = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    if status != OK:
+        _check(status, where)
+    if sync_status:
+        _check(pararnn_status_sync(workspace, handle), where + " (device status)")
 
 
-def _status(workspace, px, stream, where):
-    import torch
-
-    with torch.cuda.device(px.device):
-        st = stream if stream is not None else torch.cuda.current_stream(px.device)
-        _check(pararnn_status_sync(workspace, st), where + " (device status)")
-
-
-def _header(workspace, sync_status, device):
+def _header(workspace, sync_status, like):
     """The workspace of a call that needs one only to record its status."""
     import torch
 
     if workspace is None and sync_status:
-        return torch.empty(256, dtype=torch.uint8, device=device)
+        return torch.empty(256, dtype=torch.uint8, device=like.device)
     return workspace
 
 
 def _scan_shape(px, lam, ndim):
     import torch
 
-    if px.dim() != ndim or px.shape[-2] != 3:
-        raise ValueError("preacts must be (%s3, D), got %s" % ("B, T, " if ndim == 4 else "N, ", tuple(px.shape)))
-    _expect("lam", lam, (px.shape[-1],), torch.float32)
-    return _dtype_code(px)
+    shape = px.shape
+    if len(shape) != ndim or shape[-2] != 3:
+        raise ValueError("preacts must be (%s3, D), got %s" % ("B, T, " if ndim == 4 else "N, ", tuple(shape)))
+    _expect("lam", lam, (shape[-1],), torch.float32)
+    return _dtype_code(px), shape
 
 
 def _mask(reset, B, T):
@@ -585,25 +591,19 @@ def gated_scan_forward(px, lam, decay=8.0, h0=None, reset=None, want_grad=False,
     its status only in a workspace (>= 256 bytes) that is passed."""
     import torch
 
-    code = _scan_shape(px, lam, 4)
-    B, T, _, D = px.shape
+    code, (B, T, _, D) = _scan_shape(px, lam, 4)
     reset = _mask(reset, B, T)
     _expect("h0", h0, (B, D), torch.float32)
     _expect("out", out, (B, T, D), px.dtype)
     _expect("h_last", h_last, (B, D), torch.float32)
-    _same_device(px, lam, h0, reset, out, h_last, workspace)
-    H = torch.empty((B, T, D), dtype=px.dtype, device=px.device) if out is None else out
-    last = torch.empty((B, D), dtype=torch.float32, device=px.device) if h_last is None else h_last
-    ck = None
-    if want_grad:
-        n = pararnn_gated_scan_checkpoint_bytes(B, T, D, code)
-        ck = torch.empty(n // 4, dtype=torch.float32, device=px.device)
-    ws = _header(workspace, sync_status, px.device)
-    _check(_launch(lambda st: pararnn_gated_scan_forward(B, T, D, code, px, lam, decay, h0, reset, H, last, ck, ws,
-                                                         ws.numel() * ws.element_size() if ws is not None else 0, st),
-                   px, stream, (H, last, ck, ws)), "pararnn_gated_scan_forward")
-    if sync_status:
-        _status(ws, px, stream, "pararnn_gated_scan_forward")
+    dev = _same_device(px, lam, h0, reset, out, h_last, workspace)
+    H = px.new_empty((B, T, D)) if out is None else out
+    last = lam.new_empty((B, D)) if h_last is None else h_last
+    ck = lam.new_empty(pararnn_gated_scan_checkpoint_bytes(B, T, D, code) // 4) if want_grad else None
+    ws = _header(workspace, sync_status, px)
+    _launch("pararnn_gated_scan_forward", load().pararnn_gated_scan_forward, dev, stream, (H, last, ck, ws), ws,
+            sync_status, (B, T, D, code, px.data_ptr(), lam.data_ptr(), decay, _ptr(h0), _ptr(reset), H.data_ptr(),
+                          last.data_ptr(), _ptr(ck)))
     return H, last, ck
 
 
@@ -614,25 +614,21 @@ def gated_scan_backward(px, lam, checkpoints, dL_dH, decay=8.0, reset=None, dL_d
     or None), the latter two float32.  dL_dH has px's dtype."""
     import torch
 
-    code = _scan_shape(px, lam, 4)
-    B, T, _, D = px.shape
+    code, (B, T, _, D) = _scan_shape(px, lam, 4)
     reset = _mask(reset, B, T)
     _expect("dL_dH", dL_dH, (B, T, D), px.dtype)
     _expect("dL_dh_last", dL_dh_last, (B, D), torch.float32)
     _expect("checkpoints", checkpoints, (pararnn_gated_scan_checkpoint_bytes(B, T, D, code) // 4,), torch.float32)
-    _same_device(px, lam, checkpoints, dL_dH, reset, dL_dh_last, workspace)
+    dev = _same_device(px, lam, checkpoints, dL_dH, reset, dL_dh_last, workspace)
     dpx = torch.empty_like(px)
-    dlam = torch.empty((D,), dtype=torch.float32, device=px.device) if want_dlam else None
-    dh0 = torch.empty((B, D), dtype=torch.float32, device=px.device) if want_dh0 else None
+    dlam = lam.new_empty((D,)) if want_dlam else None
+    dh0 = lam.new_empty((B, D)) if want_dh0 else None
     ws = workspace
     if ws is None:
         ws = torch.empty(pararnn_gated_scan_workspace_bytes(B, T, D), dtype=torch.uint8, device=px.device)
-    _check(_launch(lambda st: pararnn_gated_scan_backward(B, T, D, code, px, lam, decay, reset, checkpoints, dL_dH,
-                                                          dL_dh_last, dpx, dlam, dh0, ws,
-                                                          ws.numel() * ws.element_size(), st),
-                   px, stream, (dpx, dlam, dh0, ws)), "pararnn_gated_scan_backward")
-    if sync_status:
-        _status(ws, px, stream, "pararnn_gated_scan_backward")
+    _launch("pararnn_gated_scan_backward", load().pararnn_gated_scan_backward, dev, stream, (dpx, dlam, dh0, ws), ws,
+            sync_status, (B, T, D, code, px.data_ptr(), lam.data_ptr(), decay, _ptr(reset), checkpoints.data_ptr(),
+                          dL_dH.data_ptr(), _ptr(dL_dh_last), dpx.data_ptr(), _ptr(dlam), _ptr(dh0)))
     return dpx, dlam, dh0
 
 
@@ -643,47 +639,39 @@ def gated_scan_step(px, lam, state, decay=8.0, slots=None, out=None, workspace=N
     Rows that name one slot are taken in order."""
     import torch
 
-    code = _scan_shape(px, lam, 3)
-    N, _, D = px.shape
+    code, (N, _, D) = _scan_shape(px, lam, 3)
     if state.dim() != 2:
         raise ValueError("state must be (n_slots, D), got %s" % (tuple(state.shape),))
-    _expect("state", state, (state.shape[0], D), torch.float32)
+    n_slots = state.shape[0]
+    _expect("state", state, (n_slots, D), torch.float32)
     _expect("slots", slots, (N,), torch.int32)
     _expect("out", out, (N, D), px.dtype)
-    _same_device(px, lam, state, slots, out, workspace)
+    dev = _same_device(px, lam, state, slots, out, workspace)
     y = out
     if y is None:
-        make = torch.empty if slots is None else torch.zeros
-        y = make((N, D), dtype=px.dtype, device=px.device)
-    ws = _header(workspace, sync_status, px.device)
-    _check(_launch(lambda st: pararnn_gated_scan_step(N, D, code, px, lam, decay, state.shape[0], slots, state, y, ws,
-                                                      ws.numel() * ws.element_size() if ws is not None else 0, st),
-                   px, stream, (y, ws)), "pararnn_gated_scan_step")
-    if sync_status:
-        _status(ws, px, stream, "pararnn_gated_scan_step")
+        y = px.new_empty((N, D)) if slots is None else px.new_zeros((N, D))
+    ws = _header(workspace, sync_status, px)
+    _launch("pararnn_gated_scan_step", load().pararnn_gated_scan_step, dev, stream, (y, ws), ws, sync_status,
+            (N, D, code, px.data_ptr(), lam.data_ptr(), decay, n_slots, _ptr(slots), state.data_ptr(), y.data_ptr()))
     return y
 
 
-def _norm_shape(x, *params):
-    """(M, P, N) of x for scales of shape (N,) or (P..., N), which are x's last dimensions."""
+def _norm_shape(x, shape, *params):
+    """(M, P, N) of x for scales of `shape`, (N,) or (P..., N): x's last dimensions."""
     import torch
 
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError("x must have at least one value in its last dimension, got %s" % (tuple(x.shape),))
-    shape = tuple(x.shape[-1:])
-    for t in params:
-        if t is not None:
-            shape = tuple(t.shape)
-            break
-    if not 1 <= len(shape) <= x.dim() or tuple(x.shape[x.dim() - len(shape):]) != shape or 0 in shape:
+    full, n = x.shape, len(shape)
+    if not full or full[-1] == 0:
+        raise ValueError("x must have at least one value in its last dimension, got %s" % (tuple(full),))
+    if not 1 <= n <= len(full) or full[len(full) - n:] != shape or 0 in shape:
         raise ValueError("weight and bias must have the shape of x's last dimensions, got %s for %s"
-                         % (shape, tuple(x.shape)))
+                         % (tuple(shape), tuple(full)))
     for t in params:
         _expect("weight and bias", t, shape, torch.float32)
-    P = 1
-    for n in shape[:-1]:
-        P *= n
-    return x.numel() // (P * shape[-1]), P, shape[-1], shape
+    P, N = 1, shape[-1]
+    for k in shape[:-1]:
+        P *= k
+    return x.numel() // (P * N), P, N
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, workspace=None, stream=None,
@@ -696,20 +684,19 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, want_stats=False, ou
     import torch
 
     code = _dtype_code(x)
-    M, P, N, _ = _norm_shape(x, weight, bias)
+    like = weight if weight is not None else bias
+    M, P, N = _norm_shape(x, x.shape[-1:] if like is None else like.shape, weight, bias)
     _expect("out", out, x.shape, x.dtype)
-    _same_device(x, weight, bias, out, workspace)
+    dev = _same_device(x, weight, bias, out, workspace)
     y = torch.empty_like(x) if out is None else out
     mean = rstd = None
     if want_stats:
-        mean = torch.empty(tuple(x.shape[:-1]), dtype=torch.float32, device=x.device)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-    ws = _header(workspace, sync_status, x.device)
-    _check(_launch(lambda st: pararnn_layer_norm_forward(M, P, N, code, x, weight, bias, eps, y, mean, rstd, ws,
-                                                         ws.numel() * ws.element_size() if ws is not None else 0, st),
-                   x, stream, (y, mean, rstd, ws)), "pararnn_layer_norm_forward")
-    if sync_status:
-        _status(ws, x, stream, "pararnn_layer_norm_forward")
+    ws = _header(workspace, sync_status, x)
+    _launch("pararnn_layer_norm_forward", load().pararnn_layer_norm_forward, dev, stream, (y, mean, rstd, ws), ws,
+            sync_status, (M, P, N, code, x.data_ptr(), _ptr(weight), _ptr(bias), eps, y.data_ptr(), _ptr(mean),
+                          _ptr(rstd)))
     return y, mean, rstd
 
 
@@ -721,24 +708,19 @@ def layer_norm_backward(x, dL_dy, mean, rstd, weight=None, param_shape=None, wan
     import torch
 
     code = _dtype_code(x)
-    if weight is None and param_shape is not None:
-        weight_like = torch.empty(tuple(param_shape), dtype=torch.float32, device="meta")
-    else:
-        weight_like = weight
-    M, P, N, shape = _norm_shape(x, weight_like)
+    shape = weight.shape if weight is not None else torch.Size(param_shape) if param_shape is not None else x.shape[-1:]
+    M, P, N = _norm_shape(x, shape, weight)
     _expect("dL_dy", dL_dy, x.shape, x.dtype)
     _expect("mean", mean, x.shape[:-1], torch.float32)
     _expect("rstd", rstd, x.shape[:-1], torch.float32)
-    _same_device(x, dL_dy, mean, rstd, weight, workspace)
+    dev = _same_device(x, dL_dy, mean, rstd, weight, workspace)
     dx = torch.empty_like(x)
     dw = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dparams else None
-    db = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dparams else None
+    db = torch.empty_like(dw) if want_dparams else None
     ws = workspace
     if ws is None:
         ws = torch.empty(pararnn_layer_norm_workspace_bytes(M, P, N), dtype=torch.uint8, device=x.device)
-    _check(_launch(lambda st: pararnn_layer_norm_backward(M, P, N, code, x, weight, mean, rstd, dL_dy, dx, dw, db, ws,
-                                                          ws.numel() * ws.element_size(), st),
-                   x, stream, (dx, dw, db, ws)), "pararnn_layer_norm_backward")
-    if sync_status:
-        _status(ws, x, stream, "pararnn_layer_norm_backward")
+    _launch("pararnn_layer_norm_backward", load().pararnn_layer_norm_backward, dev, stream, (dx, dw, db, ws), ws,
+            sync_status, (M, P, N, code, x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+                          dL_dy.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db)))
     return dx, dw, db

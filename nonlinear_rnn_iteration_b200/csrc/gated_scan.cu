@@ -111,15 +111,16 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // steps.  The last warp forms the carry of the next tile.  In a cluster the last warp
 // first sends the tile's element into every block's shared memory, where an
 // mbarrier counts the bytes: no block waits for more than the data it needs.
-// Every pre-activation is read once, by tensor copies two or more tiles ahead.
+// Every pre-activation is read once, by tensor copies two tiles ahead; where rows or
+// buffers are not multiples of 16 bytes (kTma false) each thread loads its own values.
 constexpr int kW = 64;  // channels per block
 constexpr int kMaxRanks = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <typename T, bool kForward>
+template <typename T, bool kForward, bool kTma>
 struct Tile {
     // the forward of bfloat16 has the registers and the stages for 16 steps a thread
-    static constexpr int R = kForward && sizeof(T) == 2 ? 16 : kCkSteps;
+    static constexpr int R = kForward && kTma && sizeof(T) == 2 ? 16 : kCkSteps;
     static constexpr int NW = 8;  // warps per block
     static constexpr int L = NW * R;
 };
@@ -146,14 +147,14 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
     return o;
 }
 
-template <typename T>
+template <typename T, bool kTma>
 struct FwdSmem {
-    static constexpr int kStages = 2;
-    alignas(128) T px[kStages][Tile<T, true>::L][3][kW];
-    float4 warp[2][Tile<T, true>::NW][32];  // each warp's element, two rounds in turn
+    static constexpr int kStages = kTma ? 2 : 0;
+    alignas(128) T px[kTma ? kStages : 1][kTma ? Tile<T, true, kTma>::L : 1][3][kW];
+    float4 warp[2][Tile<T, true, kTma>::NW][32];  // each warp's element, two rounds in turn
     float4 rank[2][kMaxRanks][32];  // each of the cluster's tiles
     float2 carry[2][32];            // the state before the round
-    uint64_t bar[kStages], rank_bar[2];
+    uint64_t bar[kStages + 1], rank_bar[2];
 };
 
 __device__ __forceinline__ f2 ld2(const float* p) {
@@ -163,6 +164,10 @@ __device__ __forceinline__ f2 ld2(const float* p) {
 __device__ __forceinline__ f2 ld2(const bf16* p) {
     const unsigned v = *reinterpret_cast<const unsigned*>(p);
     return f2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+template <typename T>
+__device__ __forceinline__ f2 load_pair(const T* p, bool in0, bool in1) {
+    return f2{in0 ? PxTraits<T>::cvt(p[0]) : 0.0f, in1 ? PxTraits<T>::cvt(p[1]) : 0.0f};
 }
 __device__ __forceinline__ void st2(float* p, f2 v) { *reinterpret_cast<float2*>(p) = make_float2(v.x, v.y); }
 __device__ __forceinline__ void st2(bf16* p, f2 v) {
@@ -264,10 +269,10 @@ __device__ __forceinline__ void eval2(f2 y, f2 pi, f2 x, f2& a, f2& u) {
 }
 
 template <typename T, bool kTma, bool kCluster, bool kCuts>
-__global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
-    constexpr int kStages = FwdSmem<T>::kStages, R = Tile<T, true>::R, L = Tile<T, true>::L, kNW = Tile<T, true>::NW;
+__global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
+    constexpr int kStages = FwdSmem<T, kTma>::kStages, R = Tile<T, true, kTma>::R, L = Tile<T, true, kTma>::L, kNW = Tile<T, true, kTma>::NW;
     extern __shared__ unsigned char raw[];
-    FwdSmem<T>& sm = *reinterpret_cast<FwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+    FwdSmem<T, kTma>& sm = *reinterpret_cast<FwdSmem<T, kTma>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // one value for the warp
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
@@ -304,11 +309,13 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
         __syncthreads();
     }
     auto issue = [&](int round) {
-        const int t0 = (round * C + (int)rank) * L;
-        if (round < rounds && t0 < T_) {
-            uint64_t* bar = &sm.bar[round % kStages];
-            mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
-            tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, b);
+        if constexpr (kTma) {
+            const int t0 = (round * C + (int)rank) * L;
+            if (round < rounds && t0 < T_) {
+                uint64_t* bar = &sm.bar[round % kStages];
+                mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
+                tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, b);
+            }
         }
     };
     if (kTma && tid == 0)
@@ -320,6 +327,14 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
     };
     unsigned mark = kCuts ? marks_of(0) : 0u;
     bool late = false, bad = false;
+    auto put = [&](T* o, f2 h) {
+        if constexpr (kTma) {
+            if (in0) st2(o, h);
+        } else {
+            if (in0) o[0] = to_out<T>(h.x);
+            if (in1) o[1] = to_out<T>(h.y);
+        }
+    };
     auto keep = [&](int i, f2 h) {
         float* o = pr.ck + ((int64_t)b * pr.nCk + i) * D + d;
         if (in0) o[0] = h.x;
@@ -329,42 +344,38 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
     T* H = static_cast<T*>(pr.H) + ((int64_t)b * T_ + t0) * D;
 
     for (int round = 0; round < rounds; ++round) {
-        const int par = round & 1, st = kTma ? round % kStages : 0, tile0 = t0 - warp * R;
+        const int par = round & 1, tile0 = t0 - warp * R;
+        int st = 0;
+        if constexpr (kTma) st = round % kStages;
         unsigned marks = 0;
         if constexpr (kCuts) {
             marks = __ballot_sync(0xffffffffu, mark != 0);
             mark = marks_of(round + 1);
         }
-        if (tile0 < T_) {
-            if constexpr (kTma) {
-                wait_bar<false>(&sm.bar[st], (round / kStages) & 1, late);
-            } else {
-                for (int i = tid; i < L * 3 * kW; i += kNW * 32) {
-                    const int row = i / (3 * kW), g = (i / kW) % 3, c = i % kW, t = tile0 + row;
-                    sm.px[0][row][g][c] = (t < T_ && d0 + c < D) ? px[((int64_t)t * 3 + g) * D + d0 + c] : T(0.0f);
-                }
-                __syncthreads();
-            }
-        }
+        if constexpr (kTma)
+            if (tile0 < T_) wait_bar<false>(&sm.bar[st], (round / kStages) & 1, late);
         f2 a[R], u[R];
         Elem e{splat2(1.0f), splat2(0.0f)};
         if (t0 < T_) {
-            const T* p = &sm.px[st][warp * R][0][2 * lane];
+            // gate g of step j
+            auto at = [&](int j, int g) -> f2 {
+                if constexpr (kTma) return ld2(&sm.px[st][warp * R + j][g][2 * lane]);
+                return load_pair(px + ((int64_t)(t0 + j) * 3 + g) * D + d, in0 && t0 + j < T_, in1 && t0 + j < T_);
+            };
             float most = 0.0f;
             if (!wide) {
 #pragma unroll
                 for (int j = 0; j < R; j += 2) {
                     f2 y0, y1;
-                    decay_exponents(ld2(p + j * 3 * kW), ld2(p + (j * 3 + 3) * kW), k, y0, y1, most);
-                    eval2<false>(y0, ld2(p + (j * 3 + 1) * kW), ld2(p + (j * 3 + 2) * kW), a[j], u[j]);
-                    eval2<false>(y1, ld2(p + (j * 3 + 4) * kW), ld2(p + (j * 3 + 5) * kW), a[j + 1], u[j + 1]);
+                    decay_exponents(at(j, 0), at(j + 1, 0), k, y0, y1, most);
+                    eval2<false>(y0, at(j, 1), at(j, 2), a[j], u[j]);
+                    eval2<false>(y1, at(j + 1, 1), at(j + 1, 2), a[j + 1], u[j + 1]);
                 }
             }
             if (wide || __any_sync(0xffffffffu, most > kProduct)) {
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    eval2<true>(mul2(k, sigmoid2(ld2(p + j * 3 * kW))), ld2(p + (j * 3 + 1) * kW),
-                                ld2(p + (j * 3 + 2) * kW), a[j], u[j]);
+                    eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
             }
             e = Elem{a[0], u[0]};
             if (!kCuts || marks == 0) {
@@ -425,12 +436,12 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
             if (pr.ck) keep(t0 / kCkSteps, h);
             const int n = min(R, T_ - t0);
             T* o = H + d;
-            if (kTma && (!kCuts || marks == 0) && n == R) {
+            if ((!kCuts || marks == 0) && n == R) {
 #pragma unroll
                 for (int j = 0; j < R; ++j) {
                     if (j && j % kCkSteps == 0 && pr.ck) keep((t0 + j) / kCkSteps, h);
                     h = fma2(a[j], h, u[j]);
-                    if (in0) st2(o, h);
+                    put(o, h);
                     o += D;
                 }
             } else {
@@ -444,9 +455,7 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
                         } else {
                             h = fma2(a[j], h, u[j]);
                         }
-                        if (kTma && in0) st2(o, h);
-                        if (!kTma && in0) o[0] = to_out<T>(h.x);
-                        if (!kTma && in1) o[1] = to_out<T>(h.y);
+                        put(o, h);
                         o += D;
                     }
             }
@@ -480,16 +489,17 @@ __global__ void __launch_bounds__(Tile<T, true>::NW * 32, 2) forward_kernel(cons
 // steps backwards for l, then forwards from the checkpoint, the state before its
 // first step, for h_{t-1} and the gradients: of the states one in R is read, and the
 // forward's scan is not repeated.
-template <typename T>
+template <typename T, bool kTma>
 struct BwdSmem {
-    static constexpr int kA = 4 / sizeof(T), kB = kA + 1;  // stages of p_r and g, of p_i and x
-    alignas(128) T pr[kA][Tile<T, false>::L][kW];
-    alignas(128) T g[kA][Tile<T, false>::L][kW];
-    alignas(128) T ix[kB][Tile<T, false>::L][2][kW];
-    float4 warp[2][Tile<T, false>::NW][32];
+    static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? kA + 1 : 0;  // stages of p_r and g, of p_i and x
+    static constexpr int kRows = kTma ? Tile<T, false, kTma>::L : 1;
+    alignas(128) T pr[kA + !kTma][kRows][kW];
+    alignas(128) T g[kA + !kTma][kRows][kW];
+    alignas(128) T ix[kB + !kTma][kRows][2][kW];
+    float4 warp[2][Tile<T, false, kTma>::NW][32];
     float4 rank[2][kMaxRanks][32];
     float2 carry[2][32];
-    uint64_t bar_a[kA], bar_b[kB], rank_bar[2];
+    uint64_t bar_a[kA + 1], bar_b[kB + 1], rank_bar[2];
 };
 
 struct BwdMaps {
@@ -514,10 +524,10 @@ __device__ __forceinline__ void grads2(f2 y, f2 l, f2 pi, f2 x, f2 kinv, f2& h, 
 }
 
 template <typename T, bool kTma, bool kCluster, bool kCuts>
-__global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
-    constexpr int kA = BwdSmem<T>::kA, kB = BwdSmem<T>::kB, R = Tile<T, false>::R, L = Tile<T, false>::L, kNW = Tile<T, false>::NW;
+__global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
+    constexpr int kA = BwdSmem<T, kTma>::kA, kB = BwdSmem<T, kTma>::kB, R = Tile<T, false, kTma>::R, L = Tile<T, false, kTma>::L, kNW = Tile<T, false, kTma>::NW;
     extern __shared__ unsigned char raw[];
-    BwdSmem<T>& sm = *reinterpret_cast<BwdSmem<T>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+    BwdSmem<T, kTma>& sm = *reinterpret_cast<BwdSmem<T, kTma>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
@@ -560,15 +570,17 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
     auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
     const int q0 = tile_of(0) < tiles ? 0 : 1;  // the block's first tile is of this round
     auto issue_a = [&](int i) {
+        if constexpr (!kTma) return;
         if (q0 + i >= rounds) return;
-        const int t0 = tile_of(q0 + i) * L, st = i % kA;
+        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kA + !kTma) : 0;
         mbar_arrive_expect_tx(&sm.bar_a[st], (uint32_t)(L * 2 * kW * sizeof(T)));
         tma_load_4d(sm.pr[st], &maps.pr, &sm.bar_a[st], d0, 0, t0, b);
         tma_load_4d(sm.g[st], &maps.g, &sm.bar_a[st], d0, 0, t0, b);
     };
     auto issue_b = [&](int i) {
+        if constexpr (!kTma) return;
         if (q0 + i >= rounds) return;
-        const int t0 = tile_of(q0 + i) * L, st = i % kB;
+        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kB + !kTma) : 0;
         mbar_arrive_expect_tx(&sm.bar_b[st], (uint32_t)(L * 2 * kW * sizeof(T)));
         tma_load_4d(sm.ix[st], &maps.ix, &sm.bar_b[st], d0, 1, t0, b);
     };
@@ -602,41 +614,39 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
         const int par = q & 1, i = q - q0;
         const int tile0 = tile_of(q) * L, t0 = tile0 + warp * R;
         const int n = max(0, min(R, T_ - t0));  // this warp's steps
-        const int sa = kTma && i >= 0 ? i % kA : 0, sb = kTma && i >= 0 ? i % kB : 0;
+        const int sa = kTma && i >= 0 ? i % (kA + !kTma) : 0, sb = kTma && i >= 0 ? i % (kB + !kTma) : 0;
         unsigned marks = 0;
         if constexpr (kCuts) {
             marks = __ballot_sync(0xffffffffu, mark != 0);
             mark = marks_of(q + 1);
         }
-        if (i >= 0) {
-            if constexpr (kTma) {
-                wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
-            } else {
-                __syncthreads();  // the tile before has been read
-                for (int c4 = tid; c4 < L * 4 * kW; c4 += kNW * 32) {
-                    const int row = c4 / (4 * kW), g = (c4 / kW) % 4, c = c4 % kW, t = tile0 + row;
-                    T val = T(0.0f);
-                    if (t < T_ && d0 + c < D)
-                        val = g < 3 ? px[((int64_t)t * 3 + g) * D + d0 + c] : dH[(int64_t)t * D + d0 + c];
-                    T* to = g == 0 ? &sm.pr[0][row][c] : g == 3 ? &sm.g[0][row][c] : &sm.ix[0][row][g - 1][c];
-                    *to = val;
-                }
-                __syncthreads();
-            }
-        }
+        if constexpr (kTma)
+            if (i >= 0) wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
+        // p_r, g, p_i and x of step j
+        auto at_r = [&](int j) -> f2 {
+            if constexpr (kTma) return ld2(&sm.pr[sa][warp * R + j][2 * lane]);
+            return load_pair(px + (int64_t)(t0 + j) * 3 * D + d, in0, in1);
+        };
+        auto at_g = [&](int j) -> f2 {
+            if constexpr (kTma) return ld2(&sm.g[sa][warp * R + j][2 * lane]);
+            return load_pair(dH + (int64_t)(t0 + j) * D + d, in0, in1);
+        };
+        auto at_ix = [&](int j, int g) -> f2 {
+            if constexpr (kTma) return ld2(&sm.ix[sb][warp * R + j][g][2 * lane]);
+            return load_pair(px + ((int64_t)(t0 + j) * 3 + 1 + g) * D + d, in0, in1);
+        };
         // y, g and the element of mu over the warp's steps; steps past T keep mu (y = 0, g = 0)
         f2 y[R], l[R];
         Elem e{splat2(1.0f), splat2(0.0f)};
-        const bool plain = kTma && n == R && (!kCuts || marks == 0) && !wide;
+        const bool plain = n == R && (!kCuts || marks == 0) && !wide;
         float most = 0.0f;
         if (plain) {
 #pragma unroll
             for (int j = 0; j < R; j += 2)
-                decay_exponents(ld2(&sm.pr[sa][warp * R + j][2 * lane]), ld2(&sm.pr[sa][warp * R + j + 1][2 * lane]), k, y[j],
-                                y[j + 1], most);
+                decay_exponents(at_r(j), at_r(j + 1), k, y[j], y[j + 1], most);
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
+                l[j] = at_g(j);
                 f2 a, m;
                 decay2<false>(y[j], a, m);
                 e.B = mul2(a, add2(l[j], e.B));
@@ -649,8 +659,8 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
             for (int j = R - 1; j >= 0; --j) {
                 y[j] = l[j] = splat2(0.0f);
                 if (j < n) {
-                    y[j] = mul2(k, sigmoid2(ld2(&sm.pr[sa][warp * R + j][2 * lane])));
-                    l[j] = ld2(&sm.g[sa][warp * R + j][2 * lane]);
+                    y[j] = mul2(k, sigmoid2(at_r(j)));
+                    l[j] = at_g(j);
                     f2 a, m;
                     decay2<true>(y[j], a, m);
                     e.B = (marks >> j & 1) ? splat2(0.0f) : mul2(a, add2(l[j], e.B));
@@ -702,14 +712,14 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
                 sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
             }
         }
-        if (kTma && i >= 0) wait_bar<false>(&sm.bar_b[sb], (i / kB) & 1, late);
+        if constexpr (kTma)
+            if (i >= 0) wait_bar<false>(&sm.bar_b[sb], (i / kB) & 1, late);
         if (n == 0) continue;
         // l backwards from mu, then the gradients forwards from the checkpoint
         f2 h{0.0f, 0.0f}, part{0.0f, 0.0f}, dpr, dpi, dx, w;
         const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
         if (in0) h.x = ck[0];
         if (in1) h.y = ck[1];
-        const T* p = &sm.ix[sb][warp * R][0][2 * lane];
         T* o = static_cast<T*>(pr.dpx) + ((int64_t)b * T_ + t0) * 3 * D + d;
         if (plain) {
 #pragma unroll
@@ -721,7 +731,7 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
             }
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                grads2<false>(y[j], l[j], ld2(p + j * 2 * kW), ld2(p + (j * 2 + 1) * kW), kinv, h, dpr, dpi, dx, w);
+                grads2<false>(y[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                 part = add2(part, w);
                 chk = fma2(dx, splat2(0.0f), chk);
                 put(o, dpr, dpi, dx);
@@ -739,7 +749,7 @@ __global__ void __launch_bounds__(Tile<T, false>::NW * 32, 2) backward_kernel(co
             for (int j = 0; j < R; ++j) {
                 if (j < n) {
                     if (marks >> j & 1) h = splat2(0.0f);
-                    grads2<true>(y[j], l[j], ld2(p + j * 2 * kW), ld2(p + (j * 2 + 1) * kW), kinv, h, dpr, dpi, dx, w);
+                    grads2<true>(y[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                     part = add2(part, w);
                     chk = fma2(dx, splat2(0.0f), chk);
                     put(o, dpr, dpi, dx);
@@ -918,7 +928,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepParams pr)
 
 bool bad_sizes(int64_t B, int64_t T, int64_t D) {
     return B < 0 || T < 0 || D < 0 || B >= (int64_t(1) << 31) || T > (int64_t(1) << 30) || B * T >= (int64_t(1) << 31) ||
-           D >= (int64_t(1) << 31) || (double)B * T * D > 4.0e12 || (double)B * D > 1.0e11;
+           D > (int64_t(1) << 29) || (double)B * T * D > 4.0e12 || (double)B * D > 1.0e11;
 }
 int64_t n_checkpoints(int64_t T) { return (T + kCkSteps - 1) / kCkSteps; }
 
@@ -978,77 +988,81 @@ pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int
                                                                   : abi::cuda_fail(who, "kernel launch failed");
 }
 
-// calls f with three truth values as types
+// calls f with two truth values as types
 template <class F>
-void choose(bool a, bool b, bool c, F f) {
-    auto two = [&](auto x, auto y) { c ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
-    auto one = [&](auto x) { b ? two(x, std::true_type{}) : two(x, std::false_type{}); };
+void choose(bool a, bool b, F f) {
+    auto one = [&](auto x) { b ? f(x, std::true_type{}) : f(x, std::false_type{}); };
     a ? one(std::true_type{}) : one(std::false_type{});
 }
 
 // two blocks share an SM's 228 KB, of which each gives 1 KB to the system
 constexpr size_t kHalfSm = (228 * 1024) / 2 - 1024;
-static_assert(sizeof(FwdSmem<float>) + 128 <= kHalfSm && sizeof(FwdSmem<bf16>) + 128 <= kHalfSm, "two blocks per SM");
-static_assert(sizeof(BwdSmem<float>) + 128 <= kHalfSm && sizeof(BwdSmem<bf16>) + 128 <= kHalfSm, "two blocks per SM");
+static_assert(sizeof(FwdSmem<float, true>) + 128 <= kHalfSm && sizeof(FwdSmem<bf16, true>) + 128 <= kHalfSm);
+static_assert(sizeof(BwdSmem<float, true>) + 128 <= kHalfSm && sizeof(BwdSmem<bf16, true>) + 128 <= kHalfSm);
 
-template <typename T>
-pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaStream_t st) {
+// the grid of either kernel: channel groups, and blocks for each of them
+template <class P>
+bool plan(P& pr, int L, int64_t& blocks) {
     const int sms = sm_count();
-    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
-    constexpr int L = Tile<T, false>::L;
     pr.nCG = (int)((pr.D + kW - 1) / kW);
     pr.nCk = (int)n_checkpoints(pr.T);
-    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
-    pr.ranks = ranks_for(groups, tiles, sms);
-    if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
-    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.dH, 16) &&
-                     !abi::misaligned(pr.dpx, 16);
+    const int64_t groups = pr.B * pr.nCG;
+    pr.ranks = ranks_for(groups, (pr.T + L - 1) / L, sms);
+    blocks = groups * pr.ranks;
+    return sms > 0 && blocks < (int64_t(1) << 31);
+}
+
+template <typename T, bool kTma>
+pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaStream_t st) {
+    typedef Tile<T, false, kTma> Tl;
+    constexpr bool bf = sizeof(T) == 2;
+    int64_t blocks;
+    if (!plan(pr, Tl::L, blocks)) return abi::cuda_fail(who, "device query failed, or too many channel groups");
     BwdMaps maps;
     memset(&maps, 0, sizeof maps);
-    if (tma) {
-        const bool bf = sizeof(T) == 2;
-        pararnn_status s = encode_steps_map(&maps.pr, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 1, L);
-        if (s == PARARNN_OK) s = encode_steps_map(&maps.ix, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 2, L);
-        if (s == PARARNN_OK) s = encode_steps_map(&maps.g, pr.dH, bf, pr.D, 1, pr.T, pr.B, kW, 1, L);
+    pararnn_status s = PARARNN_OK;
+    if (kTma) {
+        s = encode_steps_map(&maps.pr, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 1, Tl::L);
+        if (s == PARARNN_OK) s = encode_steps_map(&maps.ix, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 2, Tl::L);
+        if (s == PARARNN_OK) s = encode_steps_map(&maps.g, pr.dH, bf, pr.D, 1, pr.T, pr.B, kW, 1, Tl::L);
         if (s != PARARNN_OK) return s;
     }
-    const size_t smem = sizeof(BwdSmem<T>) + 128;
-    const int64_t blocks = groups * pr.ranks;
-    pararnn_status s;
-    choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
-        s = launch_clusters<backward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>, Tile<T, false>::NW * 32>(
-            who, pr, maps, blocks, pr.ranks, smem, st);
+    choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) {
+        s = launch_clusters<backward_kernel<T, kTma, decltype(c)::value, decltype(m)::value>, Tl::NW * 32>(
+            who, pr, maps, blocks, pr.ranks, sizeof(BwdSmem<T, kTma>) + 128, st);
     });
     if (s != PARARNN_OK || !dlam) return s;
     dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.ranks, pr.D);
     return abi::launched(who);
 }
 
-template <typename T>
+template <typename T, bool kTma>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
-    const int sms = sm_count();
-    if (sms <= 0) return abi::cuda_fail(who, "device query failed");
-    constexpr int L = Tile<T, true>::L;
-    pr.nCG = (int)((pr.D + kW - 1) / kW);
-    pr.nCk = (int)n_checkpoints(pr.T);
-    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
-    pr.ranks = ranks_for(groups, tiles, sms);
-    if (groups * pr.ranks >= (int64_t(1) << 31)) return abi::fail(who, "too many channel groups");
-    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16);
+    typedef Tile<T, true, kTma> Tl;
+    int64_t blocks;
+    if (!plan(pr, Tl::L, blocks)) return abi::cuda_fail(who, "device query failed, or too many channel groups");
     CUtensorMap map;
     memset(&map, 0, sizeof map);
-    if (tma) {
-        const pararnn_status s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, L);
-        if (s != PARARNN_OK) return s;
-    }
-    const size_t smem = sizeof(FwdSmem<T>) + 128;
-    const int64_t blocks = groups * pr.ranks;
-    pararnn_status s;
-    choose(tma, pr.ranks > 1, pr.reset != nullptr, [&](auto t, auto c, auto m) {
-        s = launch_clusters<forward_kernel<T, decltype(t)::value, decltype(c)::value, decltype(m)::value>, Tile<T, true>::NW * 32>(
-            who, pr, map, blocks, pr.ranks, smem, st);
+    pararnn_status s = PARARNN_OK;
+    if (kTma) s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, Tl::L);
+    if (s != PARARNN_OK) return s;
+    choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) {
+        s = launch_clusters<forward_kernel<T, kTma, decltype(c)::value, decltype(m)::value>, Tl::NW * 32>(
+            who, pr, map, blocks, pr.ranks, sizeof(FwdSmem<T, kTma>) + 128, st);
     });
     return s;
+}
+
+template <typename T>
+pararnn_status launch(const char* who, const Params& pr, cudaStream_t st) {
+    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16);
+    return tma ? launch_forward<T, true>(who, pr, st) : launch_forward<T, false>(who, pr, st);
+}
+template <typename T>
+pararnn_status launch(const char* who, const BwdParams& pr, float* dlam, cudaStream_t st) {
+    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.dH, 16) &&
+                     !abi::misaligned(pr.dpx, 16);
+    return tma ? launch_backward<T, true>(who, pr, dlam, st) : launch_backward<T, false>(who, pr, dlam, st);
 }
 
 template <typename T>
@@ -1138,7 +1152,7 @@ pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, parar
     pr.T = T;
     pr.D = D;
     pr.decay = decay;
-    return dtype == PARARNN_F32 ? gs::launch_forward<float>(who, pr, st) : gs::launch_forward<gs::bf16>(who, pr, st);
+    return dtype == PARARNN_F32 ? gs::launch<float>(who, pr, st) : gs::launch<gs::bf16>(who, pr, st);
 }
 
 pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
@@ -1187,8 +1201,8 @@ pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, para
     pr.T = T;
     pr.D = D;
     pr.decay = decay;
-    return dtype == PARARNN_F32 ? gs::launch_backward<float>(who, pr, dL_dlambda, st)
-                                : gs::launch_backward<gs::bf16>(who, pr, dL_dlambda, st);
+    return dtype == PARARNN_F32 ? gs::launch<float>(who, pr, dL_dlambda, st)
+                                : gs::launch<gs::bf16>(who, pr, dL_dlambda, st);
 }
 
 pararnn_status pararnn_gated_scan_step(int64_t N, int64_t D, pararnn_dtype dtype, const void* preacts,

@@ -206,21 +206,20 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& l
         }
 }
 
-// Two channels' decay a = e^-y and m = 1 - a.  For y <= 1 m is y times the polynomial
-// of degree 6 through (1 - e^-y) / y at the seven Chebyshev points of [0, 1], off by
-// at most 2.4e-8 of it with its coefficients in float32, and a is 1 - m, rounded
-// to nearest: an error of a that leans to one side would add up over a memory of 1/m
-// steps.  kWide, for decays that reach past 1: there a is the exponential, which keeps the
-// digits of a small a.  kTiny keeps 1 - a^2 above zero where y is zero (its root, 3e-19,
-// stands for zero then).
+// Two channels' decay a = e^-y and m = 1 - a.  For y <= 1 m is y times a polynomial of
+// degree 5 for (1 - e^-y) / y, exact at 0 and fitted to [0, 1] by reweighted least squares: off by at
+// most 9.7e-8 of it there, 4e-9 below y = 1e-3.  a is 1 - m, rounded to nearest: an error
+// of a that leans to one side would add up over a memory of 1/m steps, as that of an
+// approximate exponential does.  kWide, for decays that reach past 1: there a is the
+// exponential, which keeps the digits of a small a.  kTiny keeps 1 - a^2 above zero where
+// y is zero (its root, 3e-19, stands for zero then).
 constexpr float kTiny = 1e-37f;
 template <bool kWide>
 __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
-    f2 s = fma2(y, splat2(1.29076303e-4f), splat2(-1.30077498e-3f));
-    s = fma2(y, s, splat2(8.27550516e-3f));
-    s = fma2(y, s, splat2(-4.16468494e-2f));
-    s = fma2(y, s, splat2(1.66663408e-1f));
-    s = fma2(y, s, splat2(-4.99999791e-1f));
+    f2 s = fma2(y, splat2(-9.14316508e-4f), splat2(7.84359034e-3f));
+    s = fma2(y, s, splat2(-4.14267108e-2f));
+    s = fma2(y, s, splat2(1.66614130e-1f));
+    s = fma2(y, s, splat2(-4.99996185e-1f));
     s = fma2(y, s, splat2(1.0f));
     m = fma2(y, s, splat2(kTiny));
     a = sub2(splat2(1.0f), m);
@@ -232,28 +231,6 @@ __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
     }
 }
 __device__ __forceinline__ f2 exp_neg2(f2 x) { return ex2_2(mul2(x, splat2(-kLog2e))); }
-
-// y = k sig(p) of a channel in two steps with one reciprocal (simultaneous inversion,
-// as in inv_pair): the special-function unit, 16 lanes a cycle and SM, is the
-// busiest one.  `most` collects the largest product of two denominators: past
-// kProduct the reciprocal leaves the float range and the steps are evaluated again with
-// a reciprocal each.
-constexpr float kProduct = 1e37f;
-__device__ __forceinline__ void decay_exponents(f2 p0, f2 p1, f2 k, f2& y0, f2& y1, float& most) {
-    const f2 d0 = add2(exp_neg2(p0), splat2(1.0f)), d1 = add2(exp_neg2(p1), splat2(1.0f));
-    const f2 p = mul2(d0, d1);
-    const f2 q = mul2(k, rcp_2(p));
-    most = fmaxf(most, fmaxf(p.x, p.y));
-    y0 = mul2(d1, q);
-    y1 = mul2(d0, q);
-}
-// sig of two channels with one reciprocal and capped exponents, for a factor whose rounding below 2^-62 to 2^-62 does not show
-__device__ __forceinline__ f2 sigmoid_pair_capped(f2 x) {
-    const f2 d = sig_den2(x);
-    f2 r;
-    inv_pair(d.x, d.y, r.x, r.y);
-    return r;
-}
 
 // a and u = sqrt(1 - a^2) sig(p_i) x from y.  With v = 1 - a^2 = m (1 + a) and d = 1 + e^{-p_i},
 // u = x v / sqrt(v d^2): one reciprocal square root for the root and the gate's reciprocal.
@@ -362,20 +339,12 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
                 if constexpr (kTma) return ld2(&sm.px[st][warp * R + j][g][2 * lane]);
                 return load_pair(px + ((int64_t)(t0 + j) * 3 + g) * D + d, in0 && t0 + j < T_, in1 && t0 + j < T_);
             };
-            float most = 0.0f;
             if (!wide) {
 #pragma unroll
-                for (int j = 0; j < R; j += 2) {
-                    f2 y0, y1;
-                    decay_exponents(at(j, 0), at(j + 1, 0), k, y0, y1, most);
-                    eval2<false>(y0, at(j, 1), at(j, 2), a[j], u[j]);
-                    eval2<false>(y1, at(j + 1, 1), at(j + 1, 2), a[j + 1], u[j + 1]);
-                }
-            }
-            if (wide || __any_sync(0xffffffffu, most > kProduct)) {
+                for (int j = 0; j < R; ++j) eval2<false>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < R; ++j)
-                    eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                for (int j = 0; j < R; ++j) eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
             }
             e = Elem{a[0], u[0]};
             if (!kCuts || marks == 0) {
@@ -507,12 +476,9 @@ struct BwdMaps {
 };
 
 // the gradients of one step of two channels; h is h_{t-1} in and h_t out
-template <bool kWide>
-__device__ __forceinline__ void grads2(f2 y, f2 l, f2 pi, f2 x, f2 kinv, f2& h, f2& dpr, f2& dpi, f2& dx, f2& w) {
-    f2 a, m;
-    decay2<kWide>(y, a, m);
+__device__ __forceinline__ void grads2(f2 y, f2 a, f2 m, f2 l, f2 pi, f2 x, f2 kinv, f2& h, f2& dpr, f2& dpi, f2& dx, f2& w) {
     const f2 v = fma2(m, a, m);
-    const f2 i = sigmoid_pair_capped(pi);
+    const f2 i = sigmoid2(pi);
     const f2 ib = mul2(f2{rsqrt_approx(v.x), rsqrt_approx(v.y)}, i);  // i / b
     const f2 e = mul2(ib, x);
     const f2 ah = mul2(a, h);
@@ -636,33 +602,28 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             return load_pair(px + ((int64_t)(t0 + j) * 3 + 1 + g) * D + d, in0, in1);
         };
         // y, g and the element of mu over the warp's steps; steps past T keep mu (y = 0, g = 0)
-        f2 y[R], l[R];
+        f2 y[R], l[R], m[R];  // m only where every decay is within 1
         Elem e{splat2(1.0f), splat2(0.0f)};
         const bool plain = n == R && (!kCuts || marks == 0) && !wide;
-        float most = 0.0f;
         if (plain) {
 #pragma unroll
-            for (int j = 0; j < R; j += 2)
-                decay_exponents(at_r(j), at_r(j + 1), k, y[j], y[j + 1], most);
-#pragma unroll
             for (int j = R - 1; j >= 0; --j) {
+                y[j] = mul2(k, sigmoid2(at_r(j)));
                 l[j] = at_g(j);
-                f2 a, m;
-                decay2<false>(y[j], a, m);
+                f2 a;
+                decay2<false>(y[j], a, m[j]);
                 e.B = mul2(a, add2(l[j], e.B));
                 e.P = mul2(a, e.P);
             }
-        }
-        if (!plain || __any_sync(0xffffffffu, most > kProduct)) {
-            e = Elem{splat2(1.0f), splat2(0.0f)};
+        } else {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
                 y[j] = l[j] = splat2(0.0f);
                 if (j < n) {
                     y[j] = mul2(k, sigmoid2(at_r(j)));
                     l[j] = at_g(j);
-                    f2 a, m;
-                    decay2<true>(y[j], a, m);
+                    f2 a, none;
+                    decay2<true>(y[j], a, none);
                     e.B = (marks >> j & 1) ? splat2(0.0f) : mul2(a, add2(l[j], e.B));
                     e.P = mul2(a, e.P);
                 }
@@ -724,14 +685,12 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         if (plain) {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                f2 a, m;
-                decay2<false>(y[j], a, m);
                 l[j] = add2(l[j], mu);
-                mu = mul2(a, l[j]);
+                mu = mul2(sub2(splat2(1.0f), m[j]), l[j]);
             }
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                grads2<false>(y[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
+                grads2(y[j], sub2(splat2(1.0f), m[j]), m[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                 part = add2(part, w);
                 chk = fma2(dx, splat2(0.0f), chk);
                 put(o, dpr, dpi, dx);
@@ -740,8 +699,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         } else {
 #pragma unroll
             for (int j = R - 1; j >= 0; --j) {
-                f2 a, m;
-                decay2<true>(y[j], a, m);
+                f2 a, none;
+                decay2<true>(y[j], a, none);
                 l[j] = add2(l[j], mu);
                 mu = (marks >> j & 1) ? splat2(0.0f) : mul2(a, l[j]);
             }
@@ -749,7 +708,9 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             for (int j = 0; j < R; ++j) {
                 if (j < n) {
                     if (marks >> j & 1) h = splat2(0.0f);
-                    grads2<true>(y[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
+                    f2 a, mm;
+                    decay2<true>(y[j], a, mm);
+                    grads2(y[j], a, mm, l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                     part = add2(part, w);
                     chk = fma2(dx, splat2(0.0f), chk);
                     put(o, dpr, dpi, dx);

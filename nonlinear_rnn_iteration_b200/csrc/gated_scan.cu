@@ -194,6 +194,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// a box from shared memory, a group of its own; parts of it outside the tensor are not written
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// the thread's stores have read their shared memory
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // a wait with a limit; after one that ran out of time the others are short
 template <bool kPeers>
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& late) {
@@ -460,11 +471,15 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
 // forward's scan is not repeated.
 template <typename T, bool kTma>
 struct BwdSmem {
-    static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? kA + 1 : 0;  // stages of p_r and g, of p_i and x
+    static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? 2 : 0;  // stages of p_r and g, of p_i and x
     static constexpr int kRows = kTma ? Tile<T, false, kTma>::L : 1;
+    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time: the
+    // threads' own stores of two channels, and their addresses, took a fifth of the time
+    static constexpr bool kOut = kTma && sizeof(T) == 2;
     alignas(128) T pr[kA + !kTma][kRows][kW];
     alignas(128) T g[kA + !kTma][kRows][kW];
     alignas(128) T ix[kB + !kTma][kRows][2][kW];
+    alignas(128) T out[kOut ? Tile<T, false, kTma>::NW : 1][kOut ? Tile<T, false, kTma>::R : 1][kOut ? 3 : 1][kOut ? kW : 1];
     float4 warp[2][Tile<T, false, kTma>::NW][32];
     float4 rank[2][kMaxRanks][32];
     float2 carry[2][32];
@@ -472,7 +487,7 @@ struct BwdSmem {
 };
 
 struct BwdMaps {
-    CUtensorMap pr, ix, g;  // boxes of one gate, of two gates, and of dL/dH
+    CUtensorMap pr, ix, g, out;  // boxes of one gate, of two gates, of dL/dH, and of a warp's dL/dpx
 };
 
 // the gradients of one step of two channels; h is h_{t-1} in and h_t out
@@ -563,16 +578,22 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     bool late = false;
     f2 sum{0.0f, 0.0f}, chk{0.0f, 0.0f};
 
-    auto put = [&](T* o, f2 dpr, f2 dpi, f2 dx) {
-        if constexpr (kTma) {
+    constexpr bool kOut = BwdSmem<T, kTma>::kOut;
+    auto put = [&](int j, T* o, f2 dpr, f2 dpi, f2 dx) {
+        if constexpr (kOut) {
+            T* to = &sm.out[warp][j][0][2 * lane];
+            st2(to, dpr);
+            st2(to + kW, dpi);
+            st2(to + 2 * kW, dx);
+        } else if constexpr (kTma) {
             if (in0) {
                 st2(o, dpr);
                 st2(o + D, dpi);
-                st2(o + 2 * D, dx);
+                st2(o + 2 * (int64_t)D, dx);
             }
         } else {
-            if (in0) o[0] = to_out<T>(dpr.x), o[D] = to_out<T>(dpi.x), o[2 * D] = to_out<T>(dx.x);
-            if (in1) o[1] = to_out<T>(dpr.y), o[D + 1] = to_out<T>(dpi.y), o[2 * D + 1] = to_out<T>(dx.y);
+            if (in0) o[0] = to_out<T>(dpr.x), o[D] = to_out<T>(dpi.x), o[2 * (int64_t)D] = to_out<T>(dx.x);
+            if (in1) o[1] = to_out<T>(dpr.y), o[D + 1] = to_out<T>(dpi.y), o[2 * (int64_t)D + 1] = to_out<T>(dx.y);
         }
     };
 
@@ -585,6 +606,13 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         if constexpr (kCuts) {
             marks = __ballot_sync(0xffffffffu, mark != 0);
             mark = marks_of(q + 1);
+        }
+        // the state before the warp's steps, read ahead of its use
+        f2 h{0.0f, 0.0f};
+        if (n > 0) {
+            const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
+            if (in0) h.x = ck[0];
+            if (in1) h.y = ck[1];
         }
         if constexpr (kTma)
             if (i >= 0) wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
@@ -677,10 +705,11 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             if (i >= 0) wait_bar<false>(&sm.bar_b[sb], (i / kB) & 1, late);
         if (n == 0) continue;
         // l backwards from mu, then the gradients forwards from the checkpoint
-        f2 h{0.0f, 0.0f}, part{0.0f, 0.0f}, dpr, dpi, dx, w;
-        const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
-        if (in0) h.x = ck[0];
-        if (in1) h.y = ck[1];
+        if constexpr (kOut) {
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+        }
+        f2 part{0.0f, 0.0f}, dpr, dpi, dx, w;
         T* o = static_cast<T*>(pr.dpx) + ((int64_t)b * T_ + t0) * 3 * D + d;
         if (plain) {
 #pragma unroll
@@ -693,8 +722,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
                 grads2(y[j], sub2(splat2(1.0f), m[j]), m[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                 part = add2(part, w);
                 chk = fma2(dx, splat2(0.0f), chk);
-                put(o, dpr, dpi, dx);
-                o += 3 * D;
+                put(j, o, dpr, dpi, dx);
+                o += 3 * (int64_t)D;
             }
         } else {
 #pragma unroll
@@ -713,10 +742,15 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
                     grads2(y[j], a, mm, l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                     part = add2(part, w);
                     chk = fma2(dx, splat2(0.0f), chk);
-                    put(o, dpr, dpi, dx);
+                    put(j, o, dpr, dpi, dx);
                 }
-                o += 3 * D;
+                o += 3 * (int64_t)D;
             }
+        }
+        if constexpr (kOut) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) tma_store_4d(&maps.out, sm.out[warp], d0, 0, t0, b);
         }
         sum = add2(sum, part);
         if (t0 == 0 && pr.dh0) {
@@ -725,6 +759,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             if (in1) to[1] = mu.y;
         }
     }
+    if (kOut && lane == 0) tma_store_wait_read();
     // the warps' sums of w in order; a sum that is not finite stands for a dL/dp_r that is not
     __syncthreads();  // the last round's elements have been read
     sm.warp[0][warp][lane] = make_float4(sum.x, sum.y, 0.0f, 0.0f);
@@ -986,6 +1021,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
         s = encode_steps_map(&maps.pr, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 1, Tl::L);
         if (s == PARARNN_OK) s = encode_steps_map(&maps.ix, pr.px, bf, pr.D, 3, pr.T, pr.B, kW, 2, Tl::L);
         if (s == PARARNN_OK) s = encode_steps_map(&maps.g, pr.dH, bf, pr.D, 1, pr.T, pr.B, kW, 1, Tl::L);
+        if (s == PARARNN_OK) s = encode_steps_map(&maps.out, pr.dpx, bf, pr.D, 3, pr.T, pr.B, kW, 3, Tl::R);
         if (s != PARARNN_OK) return s;
     }
     choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) {

@@ -272,10 +272,21 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     const int rounds = ((T_ + L - 1) / L + C - 1) / C;
     const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
 
+    auto issue = [&](int round) {
+        if constexpr (kTma) {
+            const int t0 = (round * C + (int)rank) * L;
+            if (round < rounds && t0 < T_) {
+                uint64_t* bar = &sm.bar[round % kStages];
+                mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
+                tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, b);
+            }
+        }
+    };
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+        for (int i = 0; i < kStages; ++i) issue(i);  // under way while the rest is set up
         if (kCluster)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
@@ -296,18 +307,6 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     } else {
         __syncthreads();
     }
-    auto issue = [&](int round) {
-        if constexpr (kTma) {
-            const int t0 = (round * C + (int)rank) * L;
-            if (round < rounds && t0 < T_) {
-                uint64_t* bar = &sm.bar[round % kStages];
-                mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
-                tma_load_4d(sm.px[round % kStages], &map, bar, d0, 0, t0, b);
-            }
-        }
-    };
-    if (kTma && tid == 0)
-        for (int i = 0; i < kStages; ++i) issue(i);
     // lane j of a warp reads the mark of the warp's step j, a round ahead
     auto marks_of = [&](int round) -> unsigned {
         const int t = (round * C + (int)rank) * L + warp * R + lane;
@@ -473,8 +472,8 @@ template <typename T, bool kTma>
 struct BwdSmem {
     static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? 2 : 0;  // stages of p_r and g, of p_i and x
     static constexpr int kRows = kTma ? Tile<T, false, kTma>::L : 1;
-    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time: the
-    // threads' own stores of two channels, and their addresses, took a fifth of the time
+    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time (8x4096x2048: 180 us,
+    // against 190 with the threads' own stores of two channels); float32 has no room for it
     static constexpr bool kOut = kTma && sizeof(T) == 2;
     alignas(128) T pr[kA + !kTma][kRows][kW];
     alignas(128) T g[kA + !kTma][kRows][kW];
@@ -521,11 +520,31 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
     const T* dH = static_cast<const T*>(pr.dH) + (int64_t)b * T_ * D;
 
+    // round q takes the cluster's tiles from the last ones on; only round 0 may have tiles past T
+    auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
+    const int q0 = tile_of(0) < tiles ? 0 : 1;  // the block's first tile is of this round
+    auto issue_a = [&](int i) {
+        if constexpr (!kTma) return;
+        if (q0 + i >= rounds) return;
+        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kA + !kTma) : 0;
+        mbar_arrive_expect_tx(&sm.bar_a[st], (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.pr[st], &maps.pr, &sm.bar_a[st], d0, 0, t0, b);
+        tma_load_4d(sm.g[st], &maps.g, &sm.bar_a[st], d0, 0, t0, b);
+    };
+    auto issue_b = [&](int i) {
+        if constexpr (!kTma) return;
+        if (q0 + i >= rounds) return;
+        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kB + !kTma) : 0;
+        mbar_arrive_expect_tx(&sm.bar_b[st], (uint32_t)(L * 2 * kW * sizeof(T)));
+        tma_load_4d(sm.ix[st], &maps.ix, &sm.bar_b[st], d0, 1, t0, b);
+    };
     if (tid == 0) {
         for (int i = 0; i < kA; ++i) mbar_init(&sm.bar_a[i], 1);
         for (int i = 0; i < kB; ++i) mbar_init(&sm.bar_b[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+        for (int i = 0; i < kA; ++i) issue_a(i);
+        for (int i = 0; i < kB; ++i) issue_b(i);
         if (kCluster)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
@@ -547,28 +566,6 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     } else {
         __syncthreads();
     }
-    // round q takes the cluster's tiles from the last ones on; only round 0 may have tiles past T
-    auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
-    const int q0 = tile_of(0) < tiles ? 0 : 1;  // the block's first tile is of this round
-    auto issue_a = [&](int i) {
-        if constexpr (!kTma) return;
-        if (q0 + i >= rounds) return;
-        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kA + !kTma) : 0;
-        mbar_arrive_expect_tx(&sm.bar_a[st], (uint32_t)(L * 2 * kW * sizeof(T)));
-        tma_load_4d(sm.pr[st], &maps.pr, &sm.bar_a[st], d0, 0, t0, b);
-        tma_load_4d(sm.g[st], &maps.g, &sm.bar_a[st], d0, 0, t0, b);
-    };
-    auto issue_b = [&](int i) {
-        if constexpr (!kTma) return;
-        if (q0 + i >= rounds) return;
-        const int t0 = tile_of(q0 + i) * L, st = kTma ? i % (kB + !kTma) : 0;
-        mbar_arrive_expect_tx(&sm.bar_b[st], (uint32_t)(L * 2 * kW * sizeof(T)));
-        tma_load_4d(sm.ix[st], &maps.ix, &sm.bar_b[st], d0, 1, t0, b);
-    };
-    if (kTma && tid == 0) {
-        for (int i = 0; i < kA; ++i) issue_a(i);
-        for (int i = 0; i < kB; ++i) issue_b(i);
-    }
     auto marks_of = [&](int q) -> unsigned {
         if (q >= rounds) return 0u;
         const int t = tile_of(q) * L + warp * R + lane;
@@ -579,6 +576,10 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     f2 sum{0.0f, 0.0f}, chk{0.0f, 0.0f};
 
     constexpr bool kOut = BwdSmem<T, kTma>::kOut;
+    // bfloat16, which waits for instructions and latency, reads the checkpoint and the warps'
+    // elements ahead (8x4096x2048: 181 us, against 210 without); float32, which waits for HBM, has no registers for that
+    // (4x32768x1024: 650 us with, 613 without)
+    constexpr bool kEarly = sizeof(T) == 2;
     auto put = [&](int j, T* o, f2 dpr, f2 dpi, f2 dx) {
         if constexpr (kOut) {
             T* to = &sm.out[warp][j][0][2 * lane];
@@ -607,13 +608,14 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             marks = __ballot_sync(0xffffffffu, mark != 0);
             mark = marks_of(q + 1);
         }
-        // the state before the warp's steps, read ahead of its use
+        // the state before the warp's steps
         f2 h{0.0f, 0.0f};
-        if (n > 0) {
+        auto read_state = [&]() {
             const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
             if (in0) h.x = ck[0];
             if (in1) h.y = ck[1];
-        }
+        };
+        if (kEarly && n > 0) read_state();
         if constexpr (kTma)
             if (i >= 0) wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
         // p_r, g, p_i and x of step j
@@ -668,12 +670,17 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         f2 mu;
         if constexpr (kCluster) {
             Elem pre{splat2(1.0f), splat2(0.0f)};
-            float4 of[kNW];
+            if constexpr (kEarly) {
+                float4 of[kNW];
 #pragma unroll
-            for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
+                for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
 #pragma unroll
-            for (int w = kNW - 1; w > 0; --w)
-                if (w > warp) pre = then<kCuts>(pre, unpack(of[w]));
+                for (int w = kNW - 1; w > 0; --w)
+                    if (w > warp) pre = then<kCuts>(pre, unpack(of[w]));
+            } else {
+#pragma unroll 1
+                for (int w = kNW - 1; w > warp; --w) pre = then<kCuts>(pre, unpack(sm.warp[par][w][lane]));
+            }
             if (warp == 0) {
                 const float4 all = pack(then<kCuts>(pre, e));
                 for (int r = 0; r < C; ++r) send16(&sm.rank[par][rank][lane], &sm.rank_bar[par], r, all);
@@ -690,12 +697,17 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             mu = apply<kCuts>(pre, mu);
         } else {
             mu = ld2(&sm.carry[par][lane].x);
-            float4 of[kNW];
+            if constexpr (kEarly) {
+                float4 of[kNW];
 #pragma unroll
-            for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
+                for (int w = 1; w < kNW; ++w) of[w] = sm.warp[par][w][lane];
 #pragma unroll
-            for (int w = kNW - 1; w > 0; --w)
-                if (w > warp) mu = apply<kCuts>(unpack(of[w]), mu);
+                for (int w = kNW - 1; w > 0; --w)
+                    if (w > warp) mu = apply<kCuts>(unpack(of[w]), mu);
+            } else {
+#pragma unroll 1
+                for (int w = kNW - 1; w > warp; --w) mu = apply<kCuts>(unpack(sm.warp[par][w][lane]), mu);
+            }
             if (warp == 0) {
                 const f2 c = apply<kCuts>(e, mu);
                 sm.carry[par ^ 1][lane] = make_float2(c.x, c.y);
@@ -709,6 +721,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             if (lane == 0) tma_store_wait_read();
             __syncwarp();
         }
+        if (!kEarly) read_state();
         f2 part{0.0f, 0.0f}, dpr, dpi, dx, w;
         T* o = static_cast<T*>(pr.dpx) + ((int64_t)b * T_ + t0) * 3 * D + d;
         if (plain) {

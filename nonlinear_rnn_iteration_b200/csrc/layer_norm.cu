@@ -271,10 +271,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                 chk = fma2(c.mask(o, e), splat2(0.0f), chk);
                 return o;
             };
+            auto value_of = [&](int e) {
+                if constexpr (kHold) {
+                    return out(e, w[e], b[e]);
+                } else {
+                    const float4 q = held[e / 2 * pr.tpr + at], r = held[quads + e / 2 * pr.tpr + at];
+                    return out(e, e & 1 ? f2{q.z, q.w} : f2{q.x, q.y}, e & 1 ? f2{r.z, r.w} : f2{r.x, r.y});
+                }
+            };
             if constexpr (V == 1) {
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
-                    const f2 o = out(e, w[e], b[e]);
+                    const f2 o = value_of(e);
                     if (c.in(2 * e)) store<T, 1>(y + 2 * e * c.dj, &o.x);
                     if (c.in(2 * e + 1)) store<T, 1>(y + (2 * e + 1) * c.dj, &o.y);
                 }
@@ -285,16 +293,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                         float o[V];
 #pragma unroll
                         for (int i = 0; i < V / 2; ++i) {
-                            const int e = k * (V / 2) + i;
-                            f2 we, be;
-                            if constexpr (kHold) {
-                                we = w[e], be = b[e];
-                            } else {
-                                const float4 q = held[e / 2 * pr.tpr + at], r = held[quads + e / 2 * pr.tpr + at];
-                                we = e & 1 ? f2{q.z, q.w} : f2{q.x, q.y};
-                                be = e & 1 ? f2{r.z, r.w} : f2{r.x, r.y};
-                            }
-                            const f2 q = out(e, we, be);
+                            const f2 q = value_of(k * (V / 2) + i);
                             o[2 * i] = q.x, o[2 * i + 1] = q.y;
                         }
                         store<T, V>(y + k * c.dj, o);
@@ -573,22 +572,23 @@ int pow2_at_least(int64_t n) {
 }
 
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
-// of float32, so that short and middle rows need no block barrier; the backward
-// pass, which holds two column sums for each value, has 8, or 16 past 2048 columns.
+// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16: 158 us with
+// 64 values and a warp per row, 270 with 8 and a block); the backward pass, which holds two
+// column sums for each value, has 8, or 16 past 256 columns (the same rows: 254 us with 16, 289 with 8).
 // With few rows the smaller count leaves more threads to each of them.  A row of 256 bytes or
 // more needs no neighbours: the block's rows then share one parameter row.
 Plan plan_of(int64_t M, int64_t P, int64_t N, int esz, bool by16, bool by4, bool forward, int sms) {
     Plan p{};
     p.vec = by16 ? 16 / esz : (esz == 2 && by4) ? 2 : 1;
     if (N > 16384) return Plan{};
-    const int most = forward && by16 ? 128 / esz : 16;
+    const int most = !forward ? 16 : esz == 2 && p.vec > 1 ? 64 : 32;
     p.each = 8;
-    if (forward && by16)
+    if (forward) {
         while (p.each < most && p.each * 32 < N && (double)M * P * N >= 768.0 * sms * p.each) p.each *= 2;
-    if (forward && by16)
         while (p.each < most && p.each * 1024 < N) p.each *= 2;
-    else if (N > 2048)
+    } else if (N > 256) {
         p.each = 16;
+    }
     p.tpr = pow2_at_least((N + p.each - 1) / p.each);
     p.threads = p.most = std::max(p.tpr, 256);
     const int groups = p.threads / p.tpr;
@@ -605,20 +605,15 @@ void with_shape(const Plan& p, F f) {
     if (p.vec == V && p.each == E && p.most == B)  \
         return f(std::integral_constant<int, V>{}, std::integral_constant<int, E / V>{}, std::integral_constant<int, B>{});
 #define PARARNN_LN_ALL(V) \
-    PARARNN_LN(V, 8, 256) PARARNN_LN(V, 16, 256) PARARNN_LN(V, 16, 512) PARARNN_LN(V, 16, 1024)
-    constexpr int full = 16 / sizeof(T);
-    if constexpr (kForward) {
-        PARARNN_LN_ALL(full)
-        PARARNN_LN(full, 8, 512)
-        PARARNN_LN(full, 8, 1024)
-        PARARNN_LN(full, 32, 256)
-        PARARNN_LN(full, 32, 512)
-        if constexpr (sizeof(T) == 2) {
-            PARARNN_LN(full, 64, 256)
-        }
-    } else {
-        PARARNN_LN_ALL(full)
+    PARARNN_LN(V, 8, 256) PARARNN_LN(V, 16, 256) PARARNN_LN(V, 16, 512) PARARNN_LN(V, 16, 1024)          \
+    if constexpr (kForward) {                                                                             \
+        PARARNN_LN(V, 8, 512) PARARNN_LN(V, 8, 1024) PARARNN_LN(V, 32, 256) PARARNN_LN(V, 32, 512)        \
+        if constexpr (sizeof(T) == 2 && V > 1) {                                                          \
+            PARARNN_LN(V, 64, 256)                                                                        \
+        }                                                                                                 \
     }
+    constexpr int full = 16 / sizeof(T);
+    PARARNN_LN_ALL(full)
     if constexpr (sizeof(T) == 2) {
         PARARNN_LN_ALL(2)
     }

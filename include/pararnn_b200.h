@@ -478,7 +478,10 @@ pararnn_status pararnn_head_gru_unroll(int64_t B, int64_t T, int64_t D, int n_he
  * workspace    NULL, and device-detected conditions are not recorded; or at least
  *              256 bytes, 16-byte aligned, any contents, for
  *              pararnn_status_sync(), which reports a NaN or Inf in H or h_last as
- *              PARARNN_ENONFINITE.
+ *              PARARNN_ENONFINITE.  With pararnn_gated_scan_workspace_bytes(B, T, D)
+ *              bytes a long sequence of few channels (B * ceil(D / 64) <= 16) is cut
+ *              into ranges that run at the same time, which joins the scan in
+ *              another order: the same result up to rounding.
  * Errors: PARARNN_EINVAL, with nothing launched, for bad sizes, dtype or decay and
  * for null, host or misaligned pointers; PARARNN_ECUDA if a launch fails. */
 size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype);

@@ -587,8 +587,9 @@ def gated_scan_forward(px, lam, decay=8.0, h0=None, reset=None, want_grad=False,
     h0 (B,D) or None, reset (B,T) bool or uint8 or None (steps that start from
     a zero state).  Returns (H (B,T,D) in px's dtype, the last state (B,D)
     float32, the checkpoints that gated_scan_backward takes, or None without
-    want_grad).  With sync_status=False the call does not wait, and records
-    its status only in a workspace (>= 256 bytes) that is passed."""
+    want_grad).  With sync_status=False the call does not wait, and its status
+    is read only from a workspace that is passed: >= 256 bytes, or
+    pararnn_gated_scan_workspace_bytes for the speed of few long channels."""
     import torch
 
     code, (B, T, _, D) = _scan_shape(px, lam, 4)
@@ -600,7 +601,10 @@ def gated_scan_forward(px, lam, decay=8.0, h0=None, reset=None, want_grad=False,
     H = px.new_empty((B, T, D)) if out is None else out
     last = lam.new_empty((B, D)) if h_last is None else h_last
     ck = lam.new_empty(pararnn_gated_scan_checkpoint_bytes(B, T, D, code) // 4) if want_grad else None
-    ws = _header(workspace, sync_status, px)
+    ws = workspace
+    if ws is None and T > 2048 and B * ((D + 63) // 64) <= 16:  # few channels: scratch to cut T into ranges
+        ws = torch.empty(pararnn_gated_scan_workspace_bytes(B, T, D), dtype=torch.uint8, device=px.device)
+    ws = _header(ws, sync_status, px)
     _launch("pararnn_gated_scan_forward", load().pararnn_gated_scan_forward, dev, stream, (H, last, ck, ws), ws,
             sync_status, (B, T, D, code, px.data_ptr(), lam.data_ptr(), decay, _ptr(h0), _ptr(reset), H.data_ptr(),
                           last.data_ptr(), _ptr(ck)))

@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -44,6 +45,8 @@ struct Params {
     int64_t B, T, D;
     int nCG, nCk;  // channel groups; checkpoints per batch row
     int ranks;         // blocks per cluster
+    int segs, seg_rounds;  // ranges of T, and the rounds of one
+    float4* elems;         // (B, segs + 1, nCG, 32): the state before the first range, and the ranges' elements
     float decay;
 };
 
@@ -55,12 +58,14 @@ struct BwdParams {
     const void* dH;
     const float* dlast;  // (B,D) or null
     void* dpx;
-    float* part;  // (B * ranks, D)
+    float* part;  // (B * segs * ranks, D)
     float* dh0;   // (B,D) or null
     unsigned* status;
     int64_t B, T, D;
     int nCG, nCk;
     int ranks;
+    int segs, seg_rounds;
+    float4* elems;  // the ranges' elements, and the state behind the last range
     float decay;
 };
 
@@ -111,7 +116,10 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // steps.  The last warp forms the carry of the next tile.  In a cluster the last warp
 // first sends the tile's element into every block's shared memory, where an
 // mbarrier counts the bytes: no block waits for more than the data it needs.
-// Every pre-activation is read once, by tensor copies two tiles ahead; where rows or
+// Where even clusters of 8 leave most of the device idle, T is cut into ranges: a first
+// launch (kSum) forms each range's element, and in the second each range's blocks start
+// from those of the ranges before it.  That reads the pre-activations twice, on many times the SMs.
+// Otherwise every pre-activation is read once, by tensor copies two tiles ahead; where rows or
 // buffers are not multiples of 16 bytes (kTma false) each thread loads its own values.
 constexpr int kW = 64;  // channels per block
 constexpr int kMaxRanks = 8;
@@ -256,7 +264,7 @@ __device__ __forceinline__ void eval2(f2 y, f2 pi, f2 x, f2& a, f2& u) {
     u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
 }
 
-template <typename T, bool kTma, bool kCluster, bool kCuts>
+template <typename T, bool kTma, bool kCluster, bool kCuts, bool kSum>
 __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
     constexpr int kStages = FwdSmem<T, kTma>::kStages, R = Tile<T, true, kTma>::R, L = Tile<T, true, kTma>::L, kNW = Tile<T, true, kTma>::NW;
     extern __shared__ unsigned char raw[];
@@ -265,16 +273,20 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // one value for the warp
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
     const int C = kCluster ? pr.ranks : 1;
-    const int group = (int)(blockIdx.x / C), b = group / pr.nCG;
-    const int d0 = (group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const int group = (int)(blockIdx.x / C), range = group / pr.nCG, cg = group - range * pr.nCG;
+    const int b = range / pr.segs, seg = range - b * pr.segs;
+    const int d0 = cg * kW, d = d0 + 2 * lane;
+    float4* elems = pr.elems + ((int64_t)(b * (pr.segs + 1)) * pr.nCG + cg) * 32 + lane;  // of this group, nCG * 32 apart
+    if (kSum && seg == pr.segs - 1) return;  // nothing starts from the last range
     const int T_ = (int)pr.T, D = (int)pr.D;
     const bool in0 = d < D, in1 = d + 1 < D;
-    const int rounds = ((T_ + L - 1) / L + C - 1) / C;
+    const int first = seg * pr.seg_rounds;  // the range's first round
+    const int rounds = min(pr.seg_rounds, ((T_ + L - 1) / L + C - 1) / C - first);
     const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
 
     auto issue = [&](int round) {
         if constexpr (kTma) {
-            const int t0 = (round * C + (int)rank) * L;
+            const int t0 = ((first + round) * C + (int)rank) * L;
             if (round < rounds && t0 < T_) {
                 uint64_t* bar = &sm.bar[round % kStages];
                 mbar_arrive_expect_tx(bar, (uint32_t)(L * 3 * kW * sizeof(T)));
@@ -296,8 +308,16 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     const bool wide = __any_sync(0xffffffffu, !(k.x <= 1.0f && k.y <= 1.0f));
     if (warp == 0) {
         f2 h{0.0f, 0.0f};
-        if (pr.h0 && in0) h.x = pr.h0[(int64_t)b * D + d];
-        if (pr.h0 && in1) h.y = pr.h0[(int64_t)b * D + d + 1];
+        if (pr.segs == 1 || kSum) {
+            if (pr.h0 && in0) h.x = pr.h0[(int64_t)b * D + d];
+            if (pr.h0 && in1) h.y = pr.h0[(int64_t)b * D + d + 1];
+            // h_last may be h0's buffer: the second launch reads this copy
+            if (kSum && seg == 0 && rank == 0) *elems = make_float4(0.0f, 0.0f, h.x, h.y);
+        } else {
+            h = unpack(*elems).B;
+#pragma unroll 4
+            for (int i = 0; i < seg; ++i) h = apply<kCuts>(unpack(elems[(int64_t)(i + 1) * pr.nCG * 32]), h);
+        }
         sm.carry[0][lane] = make_float2(h.x, h.y);
     }
     // every block has begun, and has read h0 (h_last may be the same buffer)
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     }
     // lane j of a warp reads the mark of the warp's step j, a round ahead
     auto marks_of = [&](int round) -> unsigned {
-        const int t = (round * C + (int)rank) * L + warp * R + lane;
+        const int t = ((first + round) * C + (int)rank) * L + warp * R + lane;
         return (lane < R && round < rounds && t < T_) ? pr.reset[(int64_t)b * T_ + t] : 0u;
     };
     unsigned mark = kCuts ? marks_of(0) : 0u;
@@ -327,7 +347,8 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
         if (in0) o[0] = h.x;
         if (in1) o[1] = h.y;
     };
-    int t0 = (int)rank * L + warp * R;  // the warp's first step
+    int t0 = (first * C + (int)rank) * L + warp * R;  // the warp's first step
+    Elem sum{splat2(1.0f), splat2(0.0f)};  // kSum: of the range, in the last warp
     T* H = static_cast<T*>(pr.H) + ((int64_t)b * T_ + t0) * D;
 
     for (int round = 0; round < rounds; ++round) {
@@ -388,6 +409,12 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
             }
             wait_bar<true>(&sm.rank_bar[par], (round >> 1) & 1, late);
             if (tid == 0) mbar_arrive_expect_tx(&sm.rank_bar[par], C * (uint32_t)sizeof sm.rank[0][0]);
+            if constexpr (kSum) {
+                if (warp == kNW - 1 && rank == 0)
+                    for (int r = 0; r < C; ++r) sum = then<kCuts>(sum, unpack(sm.rank[par][r][lane]));
+                t0 += C * L;
+                continue;
+            }
             h = ld2(&sm.carry[par][lane].x);
             for (int r = 0; r < (int)rank; ++r) h = apply<kCuts>(unpack(sm.rank[par][r][lane]), h);
             if (warp == kNW - 1) {
@@ -449,6 +476,7 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
         t0 += C * L;
         H += (int64_t)C * L * D;
     }
+    if (kSum && warp == kNW - 1 && rank == 0) elems[(int64_t)(seg + 1) * pr.nCG * 32] = pack(sum);
     if (pr.status) {
         const unsigned bits = (__any_sync(0xffffffffu, bad) ? kStatusNonFinite : 0u) |
                               (__any_sync(0xffffffffu, late) ? kStatusTimeout : 0u);
@@ -503,7 +531,7 @@ __device__ __forceinline__ void grads2(f2 y, f2 a, f2 m, f2 l, f2 pi, f2 x, f2 k
     h = fma2(v, e, ah);
 }
 
-template <typename T, bool kTma, bool kCluster, bool kCuts>
+template <typename T, bool kTma, bool kCluster, bool kCuts, bool kSum>
 __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_kernel(const BwdParams pr, const __grid_constant__ BwdMaps maps) {
     constexpr int kA = BwdSmem<T, kTma>::kA, kB = BwdSmem<T, kTma>::kB, R = Tile<T, false, kTma>::R, L = Tile<T, false, kTma>::L, kNW = Tile<T, false, kTma>::NW;
     extern __shared__ unsigned char raw[];
@@ -512,16 +540,20 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
     const int C = kCluster ? pr.ranks : 1;
-    const int group = (int)(blockIdx.x / C), b = group / pr.nCG;
-    const int d0 = (group - b * pr.nCG) * kW, d = d0 + 2 * lane;
+    const int group = (int)(blockIdx.x / C), range = group / pr.nCG, cg = group - range * pr.nCG;
+    const int b = range / pr.segs, seg = range - b * pr.segs;
+    const int d0 = cg * kW, d = d0 + 2 * lane;
+    float4* elems = pr.elems + ((int64_t)(b * (pr.segs + 1)) * pr.nCG + cg) * 32 + lane;  // of this group, nCG * 32 apart
+    if (kSum && seg == 0) return;  // nothing starts from the first range
     const int T_ = (int)pr.T, D = (int)pr.D;
     const bool in0 = d < D, in1 = d + 1 < D;
-    const int tiles = (T_ + L - 1) / L, rounds = (tiles + C - 1) / C;
+    const int first = seg * pr.seg_rounds;  // the range's first round in time
+    const int tiles = (T_ + L - 1) / L, rounds = min(pr.seg_rounds, (tiles + C - 1) / C - first);
     const T* px = static_cast<const T*>(pr.px) + (int64_t)b * T_ * 3 * D;
     const T* dH = static_cast<const T*>(pr.dH) + (int64_t)b * T_ * D;
 
     // round q takes the cluster's tiles from the last ones on; only round 0 may have tiles past T
-    auto tile_of = [&](int q) { return (rounds - 1 - q) * C + (int)rank; };
+    auto tile_of = [&](int q) { return (first + rounds - 1 - q) * C + (int)rank; };
     const int q0 = tile_of(0) < tiles ? 0 : 1;  // the block's first tile is of this round
     auto issue_a = [&](int i) {
         if constexpr (!kTma) return;
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
         for (int i = 0; i < kA; ++i) issue_a(i);
-        for (int i = 0; i < kB; ++i) issue_b(i);
+        for (int i = 0; i < (kSum ? 0 : kB); ++i) issue_b(i);
         if (kCluster)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
@@ -558,6 +590,9 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         f2 mu{0.0f, 0.0f};
         if (pr.dlast && in0) mu.x = pr.dlast[(int64_t)b * D + d];
         if (pr.dlast && in1) mu.y = pr.dlast[(int64_t)b * D + d + 1];
+        if (!kSum)
+#pragma unroll 4
+            for (int i = pr.segs - 1; i > seg; --i) mu = apply<kCuts>(unpack(elems[(int64_t)i * pr.nCG * 32]), mu);
         sm.carry[0][lane] = make_float2(mu.x, mu.y);
     }
     if constexpr (kCluster) {
@@ -574,6 +609,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
     unsigned mark = kCuts ? marks_of(0) : 0u;
     bool late = false;
     f2 sum{0.0f, 0.0f}, chk{0.0f, 0.0f};
+    Elem whole{splat2(1.0f), splat2(0.0f)};  // kSum: of the range, in warp 0
 
     constexpr bool kOut = BwdSmem<T, kTma>::kOut;
     // bfloat16, which waits for instructions and latency, reads the checkpoint and the warps'
@@ -615,7 +651,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             if (in0) h.x = ck[0];
             if (in1) h.y = ck[1];
         };
-        if (kEarly && n > 0) read_state();
+        if (kEarly && n > 0 && !kSum) read_state();
         if constexpr (kTma)
             if (i >= 0) wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
         // p_r, g, p_i and x of step j
@@ -665,7 +701,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         if (kTma && tid == 0 && i >= 0) {
             // this round's p_r and g have been read, and the round before is finished
             issue_a(i + kA);
-            if (i >= 1) issue_b(i - 1 + kB);
+            if (i >= 1 && !kSum) issue_b(i - 1 + kB);
         }
         f2 mu;
         if constexpr (kCluster) {
@@ -687,6 +723,11 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             }
             wait_bar<true>(&sm.rank_bar[par], (q >> 1) & 1, late);
             if (tid == 0) mbar_arrive_expect_tx(&sm.rank_bar[par], C * (uint32_t)sizeof sm.rank[0][0]);
+            if constexpr (kSum) {
+                if (warp == 0 && rank == 0)
+                    for (int r = C - 1; r >= 0; --r) whole = then<kCuts>(whole, unpack(sm.rank[par][r][lane]));
+                continue;
+            }
             mu = ld2(&sm.carry[par][lane].x);
             for (int r = C - 1; r > (int)rank; --r) mu = apply<kCuts>(unpack(sm.rank[par][r][lane]), mu);
             if (warp == 0) {
@@ -772,6 +813,16 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
             if (in1) to[1] = mu.y;
         }
     }
+    if constexpr (kSum) {
+        if (warp == 0 && rank == 0) elems[(int64_t)seg * pr.nCG * 32] = pack(whole);
+        const unsigned bits = __any_sync(0xffffffffu, late) ? kStatusTimeout : 0u;
+        if (bits && lane == 0) atomicOr(pr.status, bits);
+        if constexpr (kCluster) {
+            cluster_arrive_release();
+            cluster_wait_acquire();
+        }
+        return;
+    }
     if (kOut && lane == 0) tma_store_wait_read();
     // the warps' sums of w in order; a sum that is not finite stands for a dL/dp_r that is not
     __syncthreads();  // the last round's elements have been read
@@ -781,7 +832,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         f2 t{0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kNW; ++w) t = add2(t, unpack(sm.warp[0][w][lane]).P);
-        float* o = pr.part + ((int64_t)b * C + rank) * D + d;
+        float* o = pr.part + ((int64_t)range * C + rank) * D + d;
         if (in0) o[0] = t.x;
         if (in1) o[1] = t.y;
     }
@@ -997,6 +1048,9 @@ pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int
                                                                   : abi::cuda_fail(who, "kernel launch failed");
 }
 
+constexpr std::true_type yes{};
+constexpr std::false_type no{};
+
 // calls f with two truth values as types
 template <class F>
 void choose(bool a, bool b, F f) {
@@ -1009,15 +1063,36 @@ constexpr size_t kHalfSm = (228 * 1024) / 2 - 1024;
 static_assert(sizeof(FwdSmem<float, true>) + 128 <= kHalfSm && sizeof(FwdSmem<bf16, true>) + 128 <= kHalfSm);
 static_assert(sizeof(BwdSmem<float, true>) + 128 <= kHalfSm && sizeof(BwdSmem<bf16, true>) + 128 <= kHalfSm);
 
-// the grid of either kernel: channel groups, and blocks for each of them
+// Ranges of T: only up to kSegGroups channel groups (which bounds the workspace whatever the device
+// is), as many as bring two blocks to each SM with clusters of 8, of two rounds at least; with
+// fewer than three the second reading costs what the SMs gain.
+constexpr int kSegGroups = 16, kMaxSegs = 32;
+size_t elems_bytes(int64_t B, int64_t D) {
+    const int64_t nCG = (D + kW - 1) / kW;
+    return B * nCG <= kSegGroups ? (size_t)(B * nCG * (kMaxSegs + 1)) * 32 * sizeof(float4) : 0;
+}
+size_t part_bytes(int64_t B, int64_t D) {
+    const int64_t segs = elems_bytes(B, D) ? kMaxSegs : 1;
+    return (size_t)(B * D * segs) * kMaxRanks * sizeof(float);
+}
+
+// the grid of either kernel: channel groups, ranges of T, and blocks for each of them
 template <class P>
-bool plan(P& pr, int L, int64_t& blocks) {
+bool plan(P& pr, int L, bool may_cut, int64_t& blocks) {
     const int sms = sm_count();
     pr.nCG = (int)((pr.D + kW - 1) / kW);
     pr.nCk = (int)n_checkpoints(pr.T);
-    const int64_t groups = pr.B * pr.nCG;
-    pr.ranks = ranks_for(groups, (pr.T + L - 1) / L, sms);
-    blocks = groups * pr.ranks;
+    const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;
+    pr.ranks = ranks_for(groups, tiles, sms);
+    const int rounds = (int)((tiles + pr.ranks - 1) / pr.ranks);
+    int segs = 1;
+    if (may_cut && groups <= kSegGroups && pr.ranks == kMaxRanks) {
+        segs = (int)std::min<int64_t>(std::min<int64_t>(2 * sms / (groups * pr.ranks), rounds / 2), kMaxSegs);
+        if (segs < 3) segs = 1;
+    }
+    pr.seg_rounds = (rounds + segs - 1) / segs;
+    pr.segs = (rounds + pr.seg_rounds - 1) / pr.seg_rounds;
+    blocks = groups * pr.segs * pr.ranks;
     return sms > 0 && blocks < (int64_t(1) << 31);
 }
 
@@ -1026,7 +1101,7 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
     typedef Tile<T, false, kTma> Tl;
     constexpr bool bf = sizeof(T) == 2;
     int64_t blocks;
-    if (!plan(pr, Tl::L, blocks)) return abi::cuda_fail(who, "device query failed, or too many channel groups");
+    if (!plan(pr, Tl::L, true, blocks)) return abi::cuda_fail(who, "device query failed, or too many channel groups");
     BwdMaps maps;
     memset(&maps, 0, sizeof maps);
     pararnn_status s = PARARNN_OK;
@@ -1037,12 +1112,15 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
         if (s == PARARNN_OK) s = encode_steps_map(&maps.out, pr.dpx, bf, pr.D, 3, pr.T, pr.B, kW, 3, Tl::R);
         if (s != PARARNN_OK) return s;
     }
-    choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) {
-        s = launch_clusters<backward_kernel<T, kTma, decltype(c)::value, decltype(m)::value>, Tl::NW * 32>(
-            who, pr, maps, blocks, pr.ranks, sizeof(BwdSmem<T, kTma>) + 128, st);
-    });
+    auto launch_pass = [&](auto c, auto m, auto sum) {
+        s = launch_clusters<backward_kernel<T, kTma, decltype(c)::value, decltype(m)::value, decltype(sum)::value>,
+                            Tl::NW * 32>(who, pr, maps, blocks, pr.ranks, sizeof(BwdSmem<T, kTma>) + 128, st);
+    };
+    if (pr.segs > 1) pr.reset ? launch_pass(yes, yes, yes) : launch_pass(yes, no, yes);
+    if (s == PARARNN_OK) choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) { launch_pass(c, m, no); });
     if (s != PARARNN_OK || !dlam) return s;
-    dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.ranks, pr.D);
+    dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.segs * pr.ranks,
+                                                                           pr.D);
     return abi::launched(who);
 }
 
@@ -1050,16 +1128,19 @@ template <typename T, bool kTma>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     typedef Tile<T, true, kTma> Tl;
     int64_t blocks;
-    if (!plan(pr, Tl::L, blocks)) return abi::cuda_fail(who, "device query failed, or too many channel groups");
+    if (!plan(pr, Tl::L, pr.elems != nullptr, blocks))
+        return abi::cuda_fail(who, "device query failed, or too many channel groups");
     CUtensorMap map;
     memset(&map, 0, sizeof map);
     pararnn_status s = PARARNN_OK;
     if (kTma) s = encode_steps_map(&map, pr.px, sizeof(T) == 2, pr.D, 3, pr.T, pr.B, kW, 3, Tl::L);
     if (s != PARARNN_OK) return s;
-    choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) {
-        s = launch_clusters<forward_kernel<T, kTma, decltype(c)::value, decltype(m)::value>, Tl::NW * 32>(
-            who, pr, map, blocks, pr.ranks, sizeof(FwdSmem<T, kTma>) + 128, st);
-    });
+    auto launch_pass = [&](auto c, auto m, auto sum) {
+        s = launch_clusters<forward_kernel<T, kTma, decltype(c)::value, decltype(m)::value, decltype(sum)::value>,
+                            Tl::NW * 32>(who, pr, map, blocks, pr.ranks, sizeof(FwdSmem<T, kTma>) + 128, st);
+    };
+    if (pr.segs > 1) pr.reset ? launch_pass(yes, yes, yes) : launch_pass(yes, no, yes);
+    if (s == PARARNN_OK) choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) { launch_pass(c, m, no); });
     return s;
 }
 
@@ -1117,8 +1198,7 @@ size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, para
 
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D) {
     if (gs::bad_sizes(B, T, D)) return 0;
-    // a partial sum of dL/dlambda from each block of a cluster of up to 8
-    return kHeaderBytes + (size_t)(B * D) * gs::kMaxRanks * sizeof(float);
+    return kHeaderBytes + gs::elems_bytes(B, D) + gs::part_bytes(B, D);
 }
 
 pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
@@ -1157,6 +1237,9 @@ pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, parar
     pr.H = H_out;
     pr.last = h_last;
     pr.ck = checkpoints;
+    const size_t elems = gs::elems_bytes(B, D);
+    if (elems && workspace && ws_bytes >= kHeaderBytes + elems)
+        pr.elems = reinterpret_cast<float4*>(static_cast<char*>(workspace) + kHeaderBytes);
     pr.status = static_cast<unsigned*>(workspace);
     pr.B = B;
     pr.T = T;
@@ -1204,7 +1287,8 @@ pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, para
     pr.dH = dL_dH;
     pr.dlast = dL_dh_last;
     pr.dpx = dL_dpx;
-    pr.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeaderBytes);
+    pr.elems = reinterpret_cast<float4*>(static_cast<char*>(workspace) + kHeaderBytes);
+    pr.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeaderBytes + gs::elems_bytes(B, D));
     pr.dh0 = dL_dh0;
     pr.status = static_cast<unsigned*>(workspace);
     pr.B = B;

@@ -68,6 +68,41 @@ def test_forward_and_backward(shape, packed, dtype):
     assert none is None and torch.equal(H, H2) and torch.equal(last, last2)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("shape", [(1, 9000, 24), (1, 13001, 7), (3, 7000, 130)])
+def test_few_long_channels(shape, packed, dtype):
+    """T in ranges that run at once: within the bounds, the same bits again, and the state updated in place"""
+    B, T, D = shape
+    px, lam, h0, reset, dH, dl = make(B, T, D, dtype, packed, 300 + D)
+    if packed:  # long sequences too, across the ranges
+        reset[:, 1000:8000] = 0
+        reset[0, 5000] = 1
+    n = [f64(t) for t in (px, lam, h0, dH, dl)]
+    rs = None if reset is None else reset.cpu().numpy()
+    H, last, ck = binding.gated_scan_forward(px, lam, DECAY, h0, reset, want_grad=True)
+    dpx, dlam, dh0 = binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True)
+    Hr, lr = ref.forward(n[0], n[1], DECAY, n[2], rs)
+    eH, el = ref.forward_bound(n[0], n[1], DECAY, dtype, n[2], rs)
+    within(H, Hr, eH, "H")
+    within(last, lr, el, "h_last")
+    gp, gl, g0 = ref.backward(n[0], n[1], DECAY, n[3], n[2], rs, n[4])
+    ep, ela, e0 = ref.backward_bound(n[0], n[1], DECAY, n[3], dtype, n[2], rs, n[4])
+    within(dpx, gp, ep, "dpx")
+    within(dlam, gl, ela, "dlam")
+    within(dh0, g0, e0, "dh0")
+    state = h0.clone()
+    H2, _, _ = binding.gated_scan_forward(px, lam, DECAY, state, reset, h_last=state)
+    assert torch.equal(H, H2) and torch.equal(state, last)
+    again = binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dpx, dlam, dh0)))
+    # a workspace for the status alone: one pass, another order of joins
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    H3, last3, _ = binding.gated_scan_forward(px, lam, DECAY, h0, reset, workspace=small)
+    within(H3, Hr, eH, "H in one pass")
+    within(last3, lr, el, "h_last in one pass")
+
+
 def test_directional_difference():
     """the kernels' gradients against central differences of the 64-bit form's loss"""
     px, lam, h0, reset, dH, dl = make(2, 150, 40, "f32", True, 5)

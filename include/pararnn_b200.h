@@ -506,7 +506,8 @@ pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, parar
  *   dL_dlambda  (D)           float32, written; or NULL
  *   dL_dh0      (B, D)        float32, written; or NULL
  *   workspace   >= pararnn_gated_scan_workspace_bytes(B, T, D) bytes, 16-byte
- *               aligned, any contents
+ *               aligned, any contents; calls that overlap on the GPU, replays of
+ *               captured ones among them, need workspaces of their own
  * Errors as for the forward; a NaN or Inf in dL_dpx is recorded for
  * pararnn_status_sync(). */
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D);

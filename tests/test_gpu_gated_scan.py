@@ -316,6 +316,51 @@ def test_step_rows_of_one_slot_in_order():
     assert (state[[0, 2, 3]] == 0).all()
 
 
+def test_step_of_many_rows():
+    """more rows than one launch takes, a slot named on both sides of its end, slots off 16 bytes"""
+    N, D, n_slots = 8203, 12, 9000
+    rng = np.random.default_rng(16)
+    px = torch.from_numpy(np.clip(rng.standard_normal((N, 3, D)), -8, 8)).float().cuda()
+    lam = torch.from_numpy(rng.uniform(-6, 0, D)).float().cuda()
+    state = torch.from_numpy(rng.standard_normal((n_slots, D))).float().cuda()
+    slots = rng.permutation(n_slots)[:N].astype(np.int32)
+    slots[8191] = slots[8192] = slots[8202] = slots[17] = slots[16]
+    old = f64(state)
+    dev = torch.from_numpy(np.concatenate([[0], slots]).astype(np.int32)).cuda()[1:]
+    y = binding.gated_scan_step(px, lam, state, DECAY, dev)
+    want, new = ref.step(f64(px), f64(lam), DECAY, old, slots)
+    # five steps of the slot named five times; each step's bound is that of one step, and the decay only shrinks it
+    Hb, _ = ref.forward_bound(f64(px)[:, None], f64(lam), DECAY, "f32", np.maximum(np.abs(old[slots]), 4.0))
+    within(y, want, 5 * np.maximum(Hb[:, 0], Hb[[16, 17, 8191, 8192, 8202], 0].max()), "y")
+    within(state, new, 5 * Hb.max(), "state")
+    torch.cuda.synchronize()
+    state2 = torch.from_numpy(old).float().cuda()
+    y2 = binding.gated_scan_step(px, lam, state2, DECAY)  # without slots: row n on slot n
+    want2, new2 = ref.step(f64(px), f64(lam), DECAY, old, np.arange(N))
+    within(y2, want2, 2 * ref.forward_bound(f64(px)[:, None], f64(lam), DECAY, "f32", old[:N])[0][:, 0], "y2")
+
+
+def test_two_streams_at_once():
+    """calls that overlap on the GPU with buffers of their own give what they give alone"""
+    cases = [make(2, 3000, 200, "bf16", True, 17), make(1, 9000, 48, "f32", False, 18)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def run(c, st):
+        px, lam, h0, reset, dH, dl = c
+        H, last, ck = binding.gated_scan_forward(px, lam, DECAY, h0, reset, want_grad=True, stream=st,
+                                                 sync_status=False)
+        return (H, last) + binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True, stream=st,
+                                                       sync_status=False)
+
+    alone = [run(c, None) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(c, st) for c, st in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_step_without_slots_and_bad_slots():
     px, lam, h0, _, _, _ = make(6, 1, 64, "f32", False, 14)
     state = torch.cat([h0, h0])

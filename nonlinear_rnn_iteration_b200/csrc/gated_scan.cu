@@ -344,8 +344,12 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2) forward_kerne
     };
     auto keep = [&](int i, f2 h) {
         float* o = pr.ck + ((int64_t)b * pr.nCk + i) * D + d;
-        if (in0) o[0] = h.x;
-        if (in1) o[1] = h.y;
+        if constexpr (kTma) {
+            if (in0) st2(o, h);
+        } else {
+            if (in0) o[0] = h.x;
+            if (in1) o[1] = h.y;
+        }
     };
     int t0 = (first * C + (int)rank) * L + warp * R;  // the warp's first step
     Elem sum{splat2(1.0f), splat2(0.0f)};  // kSum: of the range, in the last warp
@@ -648,8 +652,11 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2) backward_ker
         f2 h{0.0f, 0.0f};
         auto read_state = [&]() {
             const float* ck = pr.ck + ((int64_t)b * pr.nCk + t0 / R) * D + d;
-            if (in0) h.x = ck[0];
-            if (in1) h.y = ck[1];
+            if constexpr (kTma) {
+                if (in0) h = ld2(ck);
+            } else {
+                h = load_pair(ck, in0, in1);
+            }
         };
         if (kEarly && n > 0 && !kSum) read_state();
         if constexpr (kTma)
@@ -1146,13 +1153,14 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
 
 template <typename T>
 pararnn_status launch(const char* who, const Params& pr, cudaStream_t st) {
-    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16);
+    const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.H, 16) &&
+                     !abi::misaligned(pr.ck, 8);
     return tma ? launch_forward<T, true>(who, pr, st) : launch_forward<T, false>(who, pr, st);
 }
 template <typename T>
 pararnn_status launch(const char* who, const BwdParams& pr, float* dlam, cudaStream_t st) {
     const bool tma = (pr.D * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.px, 16) && !abi::misaligned(pr.dH, 16) &&
-                     !abi::misaligned(pr.dpx, 16);
+                     !abi::misaligned(pr.dpx, 16) && !abi::misaligned(pr.ck, 8);
     return tma ? launch_backward<T, true>(who, pr, dlam, st) : launch_backward<T, false>(who, pr, dlam, st);
 }
 

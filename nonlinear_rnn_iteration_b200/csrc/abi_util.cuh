@@ -48,11 +48,38 @@ inline pararnn_status open_status(const char* who, void* workspace, size_t ws_by
     if (cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return cuda_fail(who, "workspace reset failed");
     return PARARNN_OK;
 }
-inline pararnn_status launched(const char* who) {
-    return cudaGetLastError() == cudaSuccess ? PARARNN_OK : cuda_fail(who, "kernel launch failed");
+// A launch that may begin while the stream's previous kernel is still running, if
+// that kernel allows it (follow_previous): the blocks wait for its end, and for its memory to be
+// visible, before they touch global memory, so only the launch itself overlaps.
+// `ranks` blocks form a cluster.
+template <class... P, class... A>
+pararnn_status launch(const char* who, void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int ranks,
+                      const A&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? PARARNN_OK : cuda_fail(who, "kernel launch failed");
 }
 
 }  // namespace abi
+
+// Allows the stream's next kernel to be launched, and waits for the previous one and its
+// memory; before the first access to global memory.
+__device__ __forceinline__ void follow_previous() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // rounding of a result to the type of the array it goes to
 template <typename T>

@@ -306,6 +306,9 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.bar[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+    }
+    follow_previous();
+    if (tid == 0) {
         for (int i = 0; i < kStages; ++i) issue(i);  // under way while the rest is set up
         if (kCluster)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
@@ -594,6 +597,9 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
         for (int i = 0; i < kB; ++i) mbar_init(&sm.bar_b[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
+    }
+    follow_previous();
+    if (tid == 0) {
         for (int i = 0; i < kA; ++i) issue_a(i);
         for (int i = 0; i < (kSum ? 0 : kB); ++i) issue_b(i);
         if (kCluster)
@@ -875,6 +881,7 @@ constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(kSumWarps * 32)
     dlam_kernel(const float* part, const float* lam, float* dlam, int64_t rows, int64_t D) {
     __shared__ float acc[kSumWarps][32];
+    follow_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t d = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
@@ -947,6 +954,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepParams pr)
     const int n0 = (int)blockIdx.x, N = (int)pr.N, tid = threadIdx.x;
     const int64_t D = pr.D, d = ((int64_t)blockIdx.y * kStepThreads + tid) * V;
     const bool in = d < D;
+    follow_previous();
     const int64_t slot = pr.slots ? pr.slots[n0] : n0;
     if (slot < 0 || slot >= pr.n_slots) {
         if (slot >= 0 && pr.status && tid == 0) atomicOr(pr.status, kStatusBadIndex);
@@ -1054,21 +1062,7 @@ pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int
                                size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     if (!prepare_kernel(kern, smem, done)) return abi::cuda_fail(who, "kernel attributes not accepted");
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3(kThreadCount, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, pr, map) == cudaSuccess ? PARARNN_OK
-                                                                  : abi::cuda_fail(who, "kernel launch failed");
+    return abi::launch(who, kern, dim3((unsigned)blocks), kThreadCount, smem, st, ranks, pr, map);
 }
 
 constexpr std::true_type yes{};
@@ -1142,9 +1136,8 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dlam, cudaS
     if (pr.segs > 1) pr.reset ? launch_pass(yes, yes, yes) : launch_pass(yes, no, yes);
     if (s == PARARNN_OK) choose(pr.ranks > 1, pr.reset != nullptr, [&](auto c, auto m) { launch_pass(c, m, no); });
     if (s != PARARNN_OK || !dlam) return s;
-    dlam_kernel<<<(unsigned)((pr.D + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, pr.lam, dlam, pr.B * pr.segs * pr.ranks,
-                                                                           pr.D);
-    return abi::launched(who);
+    return abi::launch(who, dlam_kernel, dim3((unsigned)((pr.D + 31) / 32)), kSumWarps * 32, 0, st, 1,
+                       (const float*)pr.part, pr.lam, dlam, pr.B * pr.segs * pr.ranks, pr.D);
 }
 
 template <typename T, bool kTma>
@@ -1191,11 +1184,8 @@ pararnn_status launch_step(const char* who, StepParams pr, cudaStream_t st) {
     for (int64_t n = 0; n < N; n += kStepRows) {
         pr.N = N - n < kStepRows ? N - n : kStepRows;
         const dim3 grid((unsigned)pr.N, (unsigned)chunks);
-        if (quads)
-            step_kernel<T, 4><<<grid, kStepThreads, 0, st>>>(pr);
-        else
-            step_kernel<T, 1><<<grid, kStepThreads, 0, st>>>(pr);
-        const pararnn_status s = abi::launched(who);
+        const pararnn_status s =
+            abi::launch(who, quads ? step_kernel<T, 4> : step_kernel<T, 1>, grid, kStepThreads, 0, st, 1, pr);
         if (s != PARARNN_OK) return s;
         pr.px = static_cast<const T*>(pr.px) + kStepRows * 3 * pr.D;
         pr.y = static_cast<T*>(pr.y) + kStepRows * pr.D;

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     constexpr bool kHold = E <= 16;
     __shared__ float buf[2][32][U];
     extern __shared__ float4 held[];
+    follow_previous();
     const Rows rows = rows_of(pr);
     const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c.N;
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     constexpr bool kHold = kThreads <= 512;
     __shared__ float buf[2][32][2 * U];
     extern __shared__ float2 sums[];  // [K * V][threads]
+    follow_previous();
     const Rows rows = rows_of(pr);
     const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c.N;
@@ -454,6 +456,7 @@ __device__ __forceinline__ float2 block_sum(float a, float b) {
 
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) forward_long(const Params pr) {
+    follow_previous();
     float chk = 0.0f;
     for (int64_t row = blockIdx.x; row < pr.M * pr.P; row += gridDim.x) {
         const T* x = static_cast<const T*>(pr.x) + row * pr.N;
@@ -484,6 +487,7 @@ __global__ void __launch_bounds__(kLongThreads) forward_long(const Params pr) {
 // be written over x or dy
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) columns_long(const BwdParams pr) {
+    follow_previous();
     const int64_t c = (int64_t)blockIdx.x * kLongThreads + threadIdx.x, C = pr.P * pr.N;
     if (c >= C) return;
     const int64_t p = c / pr.N;
@@ -501,6 +505,7 @@ __global__ void __launch_bounds__(kLongThreads) columns_long(const BwdParams pr)
 
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) dx_long(const BwdParams pr) {
+    follow_previous();
     float chk = 0.0f;
     for (int64_t row = blockIdx.x; row < pr.M * pr.P; row += gridDim.x) {
         const T* x = static_cast<const T*>(pr.x) + row * pr.N;
@@ -534,6 +539,7 @@ constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(kSumWarps * 32) reduce_kernel(const float* part, int parts, float* dw, float* db,
                                                                 int64_t C) {
     __shared__ float acc[kSumWarps][32];
+    follow_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // of 2 C columns
     float s = 0.0f;
@@ -651,18 +657,19 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const bool by4 = (pr.N * sizeof(T)) % 4 == 0 && !abi::misaligned(pr.x, 4) && !abi::misaligned(pr.y, 4);
     const Plan p = plan_of(pr.M, pr.P, pr.N, sizeof(T), by16, by4, true, sms);
     if (!p.vec) {
-        forward_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
-        return abi::launched(who);
+        return abi::launch(who, forward_long<T>, dim3((unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4)), kLongThreads, 0,
+                           st, 1, pr);
     }
     pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
     const int64_t blocks = slots_for(p, pr.M, sms, p.most == 256 ? 768 : p.most) * p.npc;
+    pararnn_status s = PARARNN_EINVAL;
     with_shape<T, true>(p, [&](auto v, auto k, auto big) {
         auto kern = forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
         const size_t smem = p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0;
         if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        kern<<<(unsigned)blocks, p.threads, smem, st>>>(pr);
+        s = abi::launch(who, kern, dim3((unsigned)blocks), p.threads, smem, st, 1, pr);
     });
-    return abi::launched(who);
+    return s;
 }
 
 template <typename T>
@@ -678,11 +685,14 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
     const Plan p = plan_of(pr.M, pr.P, pr.N, sizeof(T), ok(16), ok(4), false, sms);
     if (!sums) pr.part = nullptr;
     int64_t parts;
+    pararnn_status s = PARARNN_OK;
     if (!p.vec) {
         parts = std::min<int64_t>(max_parts(pr.M, C), 64);
         const dim3 cols((unsigned)((C + kLongThreads - 1) / kLongThreads), (unsigned)parts);
-        if (sums) columns_long<T><<<cols, kLongThreads, 0, st>>>(pr);
-        dx_long<T><<<(unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4), kLongThreads, 0, st>>>(pr);
+        if (sums) s = abi::launch(who, columns_long<T>, cols, kLongThreads, 0, st, 1, pr);
+        if (s == PARARNN_OK)
+            s = abi::launch(who, dx_long<T>, dim3((unsigned)std::min<int64_t>(pr.M * pr.P, sms * 4)), kLongThreads, 0, st,
+                            1, pr);
     } else {
         pr.tpr = p.tpr, pr.pb = p.pb, pr.gpp = p.gpp, pr.npc = p.npc;
         parts = slots_for(p, pr.M, sms, p.most == 256 ? 512 : p.most);
@@ -692,13 +702,12 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
             auto kern = backward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
             const size_t smem = sums ? (size_t)each * p.threads * sizeof(float2) : 0;
             if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            kern<<<(unsigned)(parts * p.npc), p.threads, smem, st>>>(pr);
+            s = abi::launch(who, kern, dim3((unsigned)(parts * p.npc)), p.threads, smem, st, 1, pr);
         });
     }
-    const pararnn_status s = abi::launched(who);
     if (s != PARARNN_OK || !sums) return s;
-    reduce_kernel<<<(unsigned)((2 * C + 31) / 32), kSumWarps * 32, 0, st>>>(pr.part, (int)parts, dw, db, C);
-    return abi::launched(who);
+    return abi::launch(who, reduce_kernel, dim3((unsigned)((2 * C + 31) / 32)), kSumWarps * 32, 0, st, 1,
+                       (const float*)pr.part, (int)parts, dw, db, C);
 }
 
 }  // namespace

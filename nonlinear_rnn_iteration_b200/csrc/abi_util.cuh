@@ -27,6 +27,7 @@ inline pararnn_status cuda_fail(const char* who, const char* what) {
     char buf[256];
     snprintf(buf, sizeof buf, "%s: %s", who, what);
     set_last_error(buf);
+    cudaGetLastError();  // reported here: the caller's next check of the runtime is not to find it again
     return PARARNN_ECUDA;
 }
 inline bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }

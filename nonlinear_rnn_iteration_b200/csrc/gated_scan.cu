@@ -120,7 +120,8 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // launch (kSum) forms each range's element, and in the second each range's blocks start
 // from those of the ranges before it.  That reads the pre-activations twice, on many times the SMs.
 // Otherwise every pre-activation is read once, by tensor copies two tiles ahead; where rows or
-// buffers are not multiples of 16 bytes (kTma false) each thread loads its own values.
+// buffers are not multiples of 16 bytes (kTma false) each warp copies the 16-byte granules that
+// hold its rows' pieces (RowRing).
 //
 // Measured: 4x32768x1024 float32 347 us, 6.2 TB/s, bound by HBM; bfloat16, which has half the bytes
 // for the same arithmetic, 8x4096x2048 118 us, 4.6 TB/s, and 1x131072x4096 in clusters 955 us, 4.5 TB/s,
@@ -161,10 +162,23 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
     return o;
 }
 
+// Rows that do not start on 16 bytes: each warp keeps a ring of its own pieces, kN of
+// them a round (its steps' gates), each the 16-byte granules that hold 64 channels,
+// brought by one bulk copy of one lane.  A round with a piece whose granules reach over the ends
+// of its array is marked and read from global memory directly.
+template <typename T, int kN>
+struct RowRing {
+    static constexpr int kSlots = sizeof(T) == 2 ? 2 : 1, kPitch = kW * (int)sizeof(T) + 16;
+    alignas(16) unsigned char piece[kSlots][kN][kPitch];
+    uint64_t bar[kSlots];
+};
+struct NoRing {};
+
 template <typename T, bool kTma>
 struct FwdSmem {
     static constexpr int kStages = kTma ? 2 : 0;
     alignas(128) T px[kTma ? kStages : 1][kTma ? Tile<T, true, kTma>::L : 1][3][kW];
+    std::conditional_t<kTma, NoRing, RowRing<T, 3 * kCkSteps>> ring[Tile<T, true, kTma>::NW];
     float4 warp[2][Tile<T, true, kTma>::NW][32];  // each warp's element, two rounds in turn
     float4 rank[2][kMaxRanks][32];  // each of the cluster's tiles
     float2 carry[2][32];            // the state before the round
@@ -230,6 +244,59 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& l
             return;
         }
 }
+
+template <typename T, int kN>
+struct RingState {
+    static constexpr int kSlots = RowRing<T, kN>::kSlots;
+    RowRing<T, kN>& ring;
+    unsigned marked = 0, phase = 0;  // a bit for each slot
+
+    __device__ __forceinline__ explicit RingState(RowRing<T, kN>& r, int lane) : ring(r) {
+        if (lane == 0) {
+            for (int i = 0; i < RowRing<T, kN>::kSlots; ++i) mbar_init(&ring.bar[i], 1);
+            mbar_fence_init();
+        }
+        __syncwarp();
+    }
+    // lane l brings piece l: `bytes` from src, of an array [begin, end); nothing where bytes is 0
+    __device__ __forceinline__ void fill(int slot, int lane, const void* src, int bytes, const void* begin, const void* end) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src), lo = at & ~uintptr_t(15);
+        const unsigned n = bytes ? (unsigned)((at - lo + bytes + 15) & ~uintptr_t(15)) : 0u;
+        const bool over = n && (lo < reinterpret_cast<uintptr_t>(begin) || lo + n > reinterpret_cast<uintptr_t>(end));
+        if (__any_sync(0xffffffffu, over)) {
+            marked |= 1u << slot;
+            return;
+        }
+        marked &= ~(1u << slot);
+        const unsigned all = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) mbar_arrive_expect_tx(&ring.bar[slot], all);
+        __syncwarp();
+        if (n)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(ring.piece[slot][lane])),
+                         "l"(lo), "r"(n), "r"(smem_u32(&ring.bar[slot]))
+                         : "memory");
+    }
+    // whether the slot's round is to be read from global memory; else waits for it
+    __device__ __forceinline__ bool direct(int slot, bool& late) {
+        if (marked >> slot & 1) return true;
+        wait_bar<false>(&ring.bar[slot], phase >> slot & 1, late);
+        phase ^= 1u << slot;
+        return false;
+    }
+    // channels 2 lane, 2 lane + 1 of piece i, which begins at src
+    __device__ __forceinline__ f2 read(int slot, int i, const T* src, int lane) const {
+        const T* p = reinterpret_cast<const T*>(ring.piece[slot][i] + (reinterpret_cast<uintptr_t>(src) & 15)) + 2 * lane;
+        return f2{PxTraits<T>::cvt(p[0]), PxTraits<T>::cvt(p[1])};
+    }
+};
+
+struct NoRingState {
+    static constexpr int kSlots = 0;
+    __device__ __forceinline__ NoRingState(NoRing&, int) {}
+};
+template <typename T, bool kTma, int kN>
+using RingOf = std::conditional_t<kTma, NoRingState, RingState<T, kN>>;
 
 // Two channels' decay a = e^-y and m = 1 - a.  For y <= 1 m is y times a polynomial of
 // degree 5 for (1 - e^-y) / y, exact at 0 and fitted to [0, 1] by reweighted least squares: off by at
@@ -307,6 +374,8 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
     }
+    constexpr int kSlots = RingOf<T, kTma, 3 * kCkSteps>::kSlots;
+    RingOf<T, kTma, 3 * kCkSteps> ring(sm.ring[warp], lane);
     follow_previous();
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) issue(i);  // under way while the rest is set up
@@ -363,6 +432,18 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         }
     };
     int t0 = (first * C + (int)rank) * L + warp * R;  // the warp's first step
+    auto piece = [&](int t, int j, int g) { return px + ((int64_t)(t + j) * 3 + g) * D + d0; };
+    auto fill = [&](int round) {
+        if constexpr (!kTma) {
+            const int t = ((first + round) * C + (int)rank) * L + warp * R;
+            if (round >= rounds || t >= T_) return;
+            const bool mine = lane < 3 * R && t + lane / 3 < T_;
+            const T* from = static_cast<const T*>(pr.px);
+            ring.fill(round % kSlots, lane, piece(t, lane / 3, lane % 3), mine ? min(kW, D - d0) * (int)sizeof(T) : 0, from,
+                      from + pr.B * T_ * 3 * D);
+        }
+    };
+    for (int i = 0; i < kSlots; ++i) fill(i);
     Elem sum{splat2(1.0f), splat2(0.0f)};  // kSum: of the range, in the last warp
     T* H = static_cast<T*>(pr.H) + ((int64_t)b * T_ + t0) * D;
 
@@ -380,18 +461,29 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         f2 a[R], u[R];
         Elem e{splat2(1.0f), splat2(0.0f)};
         if (t0 < T_) {
-            // gate g of step j
-            auto at = [&](int j, int g) -> f2 {
-                if constexpr (kTma) return ld2(&sm.px[st][warp * R + j][g][2 * lane]);
-                return load_pair(px + ((int64_t)(t0 + j) * 3 + g) * D + d, in0 && t0 + j < T_, in1 && t0 + j < T_);
+            // at(j, g): gate g of step j
+            auto evaluate = [&](auto at) {
+                if (!wide) {
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        eval2<false>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                }
             };
-            if (!wide) {
-#pragma unroll
-                for (int j = 0; j < R; ++j) eval2<false>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+            if constexpr (kTma) {
+                evaluate([&](int j, int g) { return ld2(&sm.px[st][warp * R + j][g][2 * lane]); });
+            } else if (const int slot = round % kSlots; ring.direct(slot, late)) {
+                evaluate([&](int j, int g) {
+                    return load_pair(piece(t0, j, g) + 2 * lane, in0 && t0 + j < T_, in1 && t0 + j < T_);
+                });
             } else {
-#pragma unroll
-                for (int j = 0; j < R; ++j) eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                evaluate([&](int j, int g) { return ring.read(slot, 3 * j + g, piece(t0, j, g), lane); });
             }
+            __syncwarp();
+            fill(round + kSlots);
             e = Elem{a[0], u[0]};
             if (!kCuts || marks == 0) {
 #pragma unroll
@@ -525,6 +617,7 @@ struct BwdSmem {
     alignas(128) T g[kA + !kTma][kRows][kW];
     alignas(128) T ix[kB + !kTma][kRows][2][kW];
     alignas(128) T out[kOut ? Tile<T, false, kTma>::NW : 1][kOut ? kCkSteps : 1][kOut ? 3 : 1][kOut ? kW : 1];
+    std::conditional_t<kTma, NoRing, RowRing<T, 4 * kCkSteps>> ring[Tile<T, false, kTma>::NW];
     float4 warp[2][Tile<T, false, kTma>::NW][32];
     float4 rank[2][kMaxRanks][32];
     float2 carry[2][32];
@@ -598,6 +691,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
     }
+    constexpr int kSlots = RingOf<T, kTma, 4 * kCkSteps>::kSlots;
+    RingOf<T, kTma, 4 * kCkSteps> ring(sm.ring[warp], lane);
     follow_previous();
     if (tid == 0) {
         for (int i = 0; i < kA; ++i) issue_a(i);
@@ -641,6 +736,23 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
     // elements ahead (8x4096x2048: 181 us, against 210 without); float32, which waits for HBM, has no registers for that
     // (4x32768x1024: 650 us with, 613 without)
     constexpr bool kEarly = sizeof(T) == 2;
+    // pieces 4 j .. 4 j + 3: the gates and dL/dH of step j
+    auto piece = [&](int t, int j, int g) {
+        return g < 3 ? px + ((int64_t)(t + j) * 3 + g) * D + d0 : dH + (int64_t)(t + j) * D + d0;
+    };
+    auto fill = [&](int q) {
+        if constexpr (!kTma) {
+            if (q < q0 || q >= rounds) return;
+            const int t = tile_of(q) * L + warp * R, g = lane & 3;
+            if (t >= T_) return;
+            const bool mine = t + lane / 4 < T_ && (!kSum || g == 0 || g == 3);
+            const T* from = static_cast<const T*>(g < 3 ? pr.px : pr.dH);
+            ring.fill((q - q0) % kSlots, lane, piece(t, lane / 4, g), mine ? min(kW, D - d0) * (int)sizeof(T) : 0, from,
+                      from + pr.B * T_ * D * (g < 3 ? 3 : 1));
+        }
+    };
+    for (int i = 0; i < kSlots; ++i) fill(q0 + i);
+
     auto put = [&](int j, T* o, f2 dpr, f2 dpi, f2 dx) {
         if constexpr (kOut) {
             T* to = &sm.out[warp][j][0][2 * lane];
@@ -683,17 +795,31 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
         if constexpr (kTma)
             if (i >= 0) wait_bar<false>(&sm.bar_a[sa], (i / kA) & 1, late);
         // p_r, g, p_i and x of step j
+        int slot = 0;
+        bool direct = false;
+        if constexpr (!kTma)
+            if (n > 0) {
+                slot = i % kSlots;
+                direct = ring.direct(slot, late);
+            }
+        auto from_ring = [&](int j, int g) -> f2 {
+            if constexpr (!kTma) {
+                if (!direct) return ring.read(slot, 4 * j + g, piece(t0, j, g), lane);
+                return load_pair(piece(t0, j, g) + 2 * lane, in0, in1);
+            }
+            return f2{0.0f, 0.0f};
+        };
         auto at_r = [&](int j) -> f2 {
             if constexpr (kTma) return ld2(&sm.pr[sa][warp * R + j][2 * lane]);
-            return load_pair(px + (int64_t)(t0 + j) * 3 * D + d, in0, in1);
+            return from_ring(j, 0);
         };
         auto at_g = [&](int j) -> f2 {
             if constexpr (kTma) return ld2(&sm.g[sa][warp * R + j][2 * lane]);
-            return load_pair(dH + (int64_t)(t0 + j) * D + d, in0, in1);
+            return from_ring(j, 3);
         };
         auto at_ix = [&](int j, int g) -> f2 {
             if constexpr (kTma) return ld2(&sm.ix[sb][warp * R + j][g][2 * lane]);
-            return load_pair(px + ((int64_t)(t0 + j) * 3 + 1 + g) * D + d, in0, in1);
+            return from_ring(j, 1 + g);
         };
         // y, g and the element of mu over the warp's steps; steps past T keep mu (y = 0, g = 0)
         f2 y[R], l[R], m[R];  // m only where every decay is within 1
@@ -754,6 +880,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
             if constexpr (kSum) {
                 if (warp == 0 && rank == 0)
                     for (int r = C - 1; r >= 0; --r) whole = then<kCuts>(whole, unpack(sm.rank[par][r][lane]));
+                __syncwarp();
+                if (i >= 0) fill(q + kSlots);
                 continue;
             }
             mu = ld2(&sm.carry[par][lane].x);
@@ -784,7 +912,10 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
         }
         if constexpr (kTma)
             if (i >= 0) wait_bar<false>(&sm.bar_b[sb], (i / kB) & 1, late);
-        if (n == 0) continue;
+        if (n == 0) {
+            if (i >= 0) fill(q + kSlots);
+            continue;
+        }
         // l backwards from mu, then the gradients forwards from the checkpoint
         if constexpr (kOut) {
             if (lane == 0) tma_store_wait_read();
@@ -829,6 +960,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
                 o += 3 * (int64_t)D;
             }
         }
+        __syncwarp();
+        fill(q + kSlots);
         if constexpr (kOut) {
             fence_async_shared();
             __syncwarp();

@@ -121,7 +121,7 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // from those of the ranges before it.  That reads the pre-activations twice, on many times the SMs.
 // Otherwise every pre-activation is read once, by tensor copies two tiles ahead; where rows or
 // buffers are not multiples of 16 bytes (kTma false) each warp copies the 16-byte granules that
-// hold its rows' pieces (RowRing).
+// hold its rows' pieces (RowRing), or reads them directly.
 //
 // Measured: 4x32768x1024 float32 347 us, 6.2 TB/s, bound by HBM; bfloat16, which has half the bytes
 // for the same arithmetic, 8x4096x2048 118 us, 4.6 TB/s, and 1x131072x4096 in clusters 955 us, 4.5 TB/s,
@@ -165,7 +165,10 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
 // Rows that do not start on 16 bytes: each warp keeps a ring of its own pieces, kN of
 // them a round (its steps' gates), each the 16-byte granules that hold 64 channels,
 // brought by one bulk copy of one lane.  A round with a piece whose granules reach over the ends
-// of its array is marked and read from global memory directly.
+// of its array is marked and read from global memory directly.  8x2000x2051 bfloat16: forward
+// 107 us, with direct loads alone 146, as two 2-byte loads stand for one of 4; adjoint 213, 268.
+// float32: adjoint of 16x1000x1001 150 us, direct 159, but forward 67.6, direct 65.5, so that pass
+// has no ring.
 template <typename T, int kN>
 struct RowRing {
     static constexpr int kSlots = sizeof(T) == 2 ? 2 : 1, kPitch = kW * (int)sizeof(T) + 16;
@@ -173,12 +176,14 @@ struct RowRing {
     uint64_t bar[kSlots];
 };
 struct NoRing {};
+template <typename T, bool kForward, bool kTma>
+constexpr bool kHasRing = !kTma && !(kForward && sizeof(T) == 4);
 
 template <typename T, bool kTma>
 struct FwdSmem {
     static constexpr int kStages = kTma ? 2 : 0;
     alignas(128) T px[kTma ? kStages : 1][kTma ? Tile<T, true, kTma>::L : 1][3][kW];
-    std::conditional_t<kTma, NoRing, RowRing<T, 3 * kCkSteps>> ring[Tile<T, true, kTma>::NW];
+    std::conditional_t<kHasRing<T, true, kTma>, RowRing<T, 3 * kCkSteps>, NoRing> ring[Tile<T, true, kTma>::NW];
     float4 warp[2][Tile<T, true, kTma>::NW][32];  // each warp's element, two rounds in turn
     float4 rank[2][kMaxRanks][32];  // each of the cluster's tiles
     float2 carry[2][32];            // the state before the round
@@ -295,8 +300,9 @@ struct NoRingState {
     static constexpr int kSlots = 0;
     __device__ __forceinline__ NoRingState(NoRing&, int) {}
 };
-template <typename T, bool kTma, int kN>
-using RingOf = std::conditional_t<kTma, NoRingState, RingState<T, kN>>;
+template <typename T, bool kForward, bool kTma>
+using RingOf =
+    std::conditional_t<kHasRing<T, kForward, kTma>, RingState<T, (kForward ? 3 : 4) * kCkSteps>, NoRingState>;
 
 // Two channels' decay a = e^-y and m = 1 - a.  For y <= 1 m is y times a polynomial of
 // degree 5 for (1 - e^-y) / y, exact at 0 and fitted to [0, 1] by reweighted least squares: off by at
@@ -374,8 +380,8 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
     }
-    constexpr int kSlots = RingOf<T, kTma, 3 * kCkSteps>::kSlots;
-    RingOf<T, kTma, 3 * kCkSteps> ring(sm.ring[warp], lane);
+    constexpr int kSlots = RingOf<T, true, kTma>::kSlots;
+    RingOf<T, true, kTma> ring(sm.ring[warp], lane);
     follow_previous();
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) issue(i);  // under way while the rest is set up
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
     int t0 = (first * C + (int)rank) * L + warp * R;  // the warp's first step
     auto piece = [&](int t, int j, int g) { return px + ((int64_t)(t + j) * 3 + g) * D + d0; };
     auto fill = [&](int round) {
-        if constexpr (!kTma) {
+        if constexpr (kHasRing<T, true, kTma>) {
             const int t = ((first + round) * C + (int)rank) * L + warp * R;
             if (round >= rounds || t >= T_) return;
             const bool mine = lane < 3 * R && t + lane / 3 < T_;
@@ -475,15 +481,22 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
             };
             if constexpr (kTma) {
                 evaluate([&](int j, int g) { return ld2(&sm.px[st][warp * R + j][g][2 * lane]); });
-            } else if (const int slot = round % kSlots; ring.direct(slot, late)) {
-                evaluate([&](int j, int g) {
-                    return load_pair(piece(t0, j, g) + 2 * lane, in0 && t0 + j < T_, in1 && t0 + j < T_);
-                });
             } else {
-                evaluate([&](int j, int g) { return ring.read(slot, 3 * j + g, piece(t0, j, g), lane); });
+                auto load = [&](int j, int g) {
+                    return load_pair(piece(t0, j, g) + 2 * lane, in0 && t0 + j < T_, in1 && t0 + j < T_);
+                };
+                if constexpr (kHasRing<T, true, kTma>) {
+                    const int slot = round % kSlots;
+                    if (ring.direct(slot, late))
+                        evaluate(load);
+                    else
+                        evaluate([&](int j, int g) { return ring.read(slot, 3 * j + g, piece(t0, j, g), lane); });
+                    __syncwarp();
+                    fill(round + kSlots);
+                } else {
+                    evaluate(load);
+                }
             }
-            __syncwarp();
-            fill(round + kSlots);
             e = Elem{a[0], u[0]};
             if (!kCuts || marks == 0) {
 #pragma unroll
@@ -617,7 +630,7 @@ struct BwdSmem {
     alignas(128) T g[kA + !kTma][kRows][kW];
     alignas(128) T ix[kB + !kTma][kRows][2][kW];
     alignas(128) T out[kOut ? Tile<T, false, kTma>::NW : 1][kOut ? kCkSteps : 1][kOut ? 3 : 1][kOut ? kW : 1];
-    std::conditional_t<kTma, NoRing, RowRing<T, 4 * kCkSteps>> ring[Tile<T, false, kTma>::NW];
+    std::conditional_t<kHasRing<T, false, kTma>, RowRing<T, 4 * kCkSteps>, NoRing> ring[Tile<T, false, kTma>::NW];
     float4 warp[2][Tile<T, false, kTma>::NW][32];
     float4 rank[2][kMaxRanks][32];
     float2 carry[2][32];
@@ -691,8 +704,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
         for (int i = 0; i < 2; ++i) mbar_init(&sm.rank_bar[i], 1);
         mbar_fence_init();
     }
-    constexpr int kSlots = RingOf<T, kTma, 4 * kCkSteps>::kSlots;
-    RingOf<T, kTma, 4 * kCkSteps> ring(sm.ring[warp], lane);
+    constexpr int kSlots = RingOf<T, false, kTma>::kSlots;
+    RingOf<T, false, kTma> ring(sm.ring[warp], lane);
     follow_previous();
     if (tid == 0) {
         for (int i = 0; i < kA; ++i) issue_a(i);

@@ -55,9 +55,11 @@ struct BwdParams {
 // its rows.  U rows are read and reduced at a time: that keeps enough bytes in flight and
 // shares a block barrier between them.  Two reductions of a row in the forward pass
 // (the variance is taken about the mean), one of two sums in the backward pass.
-// Measured: 131072x1x1024 float32 192 us forward, 5.6 TB/s, and 281 us backward, 5.7 TB/s, bound by HBM;
-// 32768x3x2048 bfloat16 158 us, 5.1 TB/s, and 254 us, 4.8 TB/s, bound by the latency of the row
-// loads, for which registers are left.
+// Measured: 131072x1x1024 float32 192 us forward, 5.6 TB/s, and 279 us backward, 5.8 TB/s, bound by HBM;
+// 32768x3x2048 bfloat16 152 us, 5.3 TB/s, and 252 us, 4.8 TB/s, bound by the latency of the row
+// loads, for which registers are left; rows of 64, 32768x8x64 bfloat16, 22 us and 34 us, bound by
+// instructions (places kept as running sums and a reciprocal root of few instructions took
+// the forward from 27).  Reading a batch ahead gained nothing forward and spilled backward (49 us).
 template <typename T, int V, int K>
 constexpr int words_of = K * (V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1);
 constexpr int batch_of(int words) { return words >= 16 ? 1 : words >= 8 ? 2 : 4; }
@@ -130,10 +132,11 @@ __device__ __forceinline__ void row_sums(float (&a)[n], int tpr, float (*buf)[32
     }
 }
 
-// the rows of this thread's group: m0, m0 + dm, ... below M with parameter row p
+// the rows of this thread's group: positions m, m + dm, ... below M with parameter row p.  Positions
+// fit 32 bits (dm is at most the threads of the device); rows and values are counted in 64.
 struct Rows {
-    int64_t p, m0, dm;
-    int64_t steps;  // of the whole block: the most rows that one of its groups has
+    int64_t p, row, drow;  // the first row, and the way to the next
+    uint32_t m, dm, steps;  // steps: of the whole block, the most rows that one of its groups has
     bool on;
 };
 template <class P>
@@ -142,10 +145,12 @@ __device__ __forceinline__ Rows rows_of(const P& pr) {
     const int64_t range = blockIdx.x % pr.npc, slot = blockIdx.x / pr.npc, slots = gridDim.x / pr.npc;
     Rows r;
     r.p = range * pr.pb + g % pr.pb;
-    r.m0 = slot * pr.gpp + g / pr.pb;
-    r.dm = slots * pr.gpp;
+    r.m = (uint32_t)(slot * pr.gpp + g / pr.pb);
+    r.dm = (uint32_t)(slots * pr.gpp);
+    r.row = (int64_t)r.m * pr.P + r.p;
+    r.drow = (int64_t)r.dm * pr.P;
     r.on = g < pr.pb * pr.gpp && r.p < pr.P;
-    r.steps = (pr.M - slot * pr.gpp + r.dm - 1) / r.dm;
+    r.steps = (uint32_t)((pr.M - slot * pr.gpp + r.dm - 1) / r.dm);
     return r;
 }
 
@@ -192,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     __shared__ float buf[2][32][U];
     extern __shared__ float4 held[];
     follow_previous();
-    const Rows rows = rows_of(pr);
+    Rows rows = rows_of(pr);
+    const uint32_t M = (uint32_t)pr.M;
     const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c.N;
     const float inv = 1.0f / (float)N;
@@ -228,14 +234,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
             }
         __syncthreads();
     }
-    for (int64_t it = 0; it < rows.steps; it += U) {
+    int64_t at0 = rows.row * N + c.j0;  // the thread's first value
+    const int64_t dat = rows.drow * N;
+    for (uint32_t it = 0; it < rows.steps; it += U) {
         Vec<T, V> v[U][K];
         float s[U], mean[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t m = rows.m0 + (it + u) * rows.dm;
-            const T* x = static_cast<const T*>(pr.x) + (m * pr.P + rows.p) * N + c.j0;
-            const bool on = rows.on && m < pr.M;
+            const T* x = static_cast<const T*>(pr.x) + at0 + u * dat;
+            const bool on = rows.on && rows.m + u * rows.dm < M;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 v[u][k] = Vec<T, V>{};
@@ -263,11 +270,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t m = rows.m0 + (it + u) * rows.dm;
-            if (!rows.on || m >= pr.M) continue;
-            const float rstd = 1.0f / sqrtf(s[u] * inv + pr.eps);
-            const int64_t row = m * pr.P + rows.p;
-            T* y = static_cast<T*>(pr.y) + row * N + c.j0;
+            if (!rows.on || rows.m + u * rows.dm >= M) continue;
+            const float rstd = rsqrtf(s[u] * inv + pr.eps);  // within 2 ulp
+            T* y = static_cast<T*>(pr.y) + at0 + u * dat;
             auto out = [&](int e, f2 we, f2 be) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd));
                 const f2 o = fma2(xh, we, be);
@@ -302,9 +307,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                         store<T, V>(y + k * c.dj, o);
                     }
             }
-            if (c.j0 == 0 && pr.mean) pr.mean[row] = mean[u];
-            if (c.j0 == 0 && pr.rstd) pr.rstd[row] = rstd;
+            if (c.j0 == 0 && pr.mean) pr.mean[rows.row + u * rows.drow] = mean[u];
+            if (c.j0 == 0 && pr.rstd) pr.rstd[rows.row + u * rows.drow] = rstd;
         }
+        rows.m += U * rows.dm;
+        rows.row += U * rows.drow;
+        at0 += U * dat;
     }
     if (pr.status && total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
 }
@@ -316,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     __shared__ float buf[2][32][2 * U];
     extern __shared__ float2 sums[];  // [K * V][threads]
     follow_previous();
-    const Rows rows = rows_of(pr);
+    Rows rows = rows_of(pr);
+    const uint32_t M = (uint32_t)pr.M;
     const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c.N;
     const float inv = 1.0f / (float)N;
@@ -335,25 +344,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = splat2(0.0f);
     if (kHold) params();
-    for (int64_t it = 0; it < rows.steps; it += U) {
+    int64_t at0 = rows.row * N + c.j0;  // the thread's first value
+    const int64_t dat = rows.drow * N;
+    for (uint32_t it = 0; it < rows.steps; it += U) {
         Vec<T, V> v[U][K], g[U][K];
         float mean[U], rstd[U], s[2 * U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t m = rows.m0 + (it + u) * rows.dm;
-            const bool on = rows.on && m < pr.M;
-            const int64_t row = on ? m * pr.P + rows.p : 0;
+            const bool on = rows.on && rows.m + u * rows.dm < M;
+            const int64_t at = at0 + u * dat;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 v[u][k] = Vec<T, V>{};
                 g[u][k] = Vec<T, V>{};
                 if (on && c.in(k)) {
-                    v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + row * N + c.j0 + k * c.dj);
-                    g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + row * N + c.j0 + k * c.dj);
+                    v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at + k * c.dj);
+                    g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + at + k * c.dj);
                 }
             }
-            mean[u] = on ? pr.mean[row] : 0.0f;
-            rstd[u] = on ? pr.rstd[row] : 0.0f;
+            mean[u] = on ? pr.mean[rows.row + u * rows.drow] : 0.0f;
+            rstd[u] = on ? pr.rstd[rows.row + u * rows.drow] : 0.0f;
         }
         if (!kHold) params();
         // rows past M hold zeros: they add nothing
@@ -375,10 +385,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t m = rows.m0 + (it + u) * rows.dm;
-            if (!rows.on || m >= pr.M) continue;
+            if (!rows.on || rows.m + u * rows.dm >= M) continue;
             const f2 m1 = splat2(s[2 * u] * inv), m2 = splat2(-s[2 * u + 1] * inv);
-            T* o = static_cast<T*>(pr.dx) + (m * pr.P + rows.p) * N + c.j0;
+            T* o = static_cast<T*>(pr.dx) + at0 + u * dat;
             auto out = [&](int e) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u]));
                 const f2 q = mul2(fma2(xh, m2, sub2(mul2(pair(g[u], e), w[e]), m1)), splat2(rstd[u]));
@@ -406,6 +415,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                     }
             }
         }
+        rows.m += U * rows.dm;
+        rows.row += U * rows.drow;
+        at0 += U * dat;
     }
     if (total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
     if (!pr.part) return;
@@ -581,7 +593,7 @@ int pow2_at_least(int64_t n) {
 }
 
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
-// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16: 158 us with
+// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16: 152 us with
 // 64 values and a warp per row, 270 with 8 and a block); the backward pass, which holds two
 // column sums for each value, has 8, or 16 past 256 columns (the same rows: 254 us with 16, 289 with 8).
 // With few rows the smaller count leaves more threads to each of them.  A row of 256 bytes or

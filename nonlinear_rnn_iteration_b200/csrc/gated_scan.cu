@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "abi_util.cuh"
+#include "bulk.cuh"
 #include "cluster.cuh"
 #include "common.cuh"
 #include "pararnn_b200.h"
@@ -130,7 +131,6 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // 928 us; with 12, 996, and with 8, 1140).
 constexpr int kW = 64;  // channels per block
 constexpr int kMaxRanks = 8;
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <typename T, bool kForward, bool kTma>
 struct Tile {
@@ -238,18 +238,6 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// a wait with a limit; after one that ran out of time the others are short
-template <bool kPeers>
-__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, bool& late) {
-    if (kPeers ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = globaltimer_ns(), limit = late ? 1000000ull : kWaitNs;
-    while (!(kPeers ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
-        if (globaltimer_ns() - t0 > limit) {
-            late = true;
-            return;
-        }
-}
-
 template <typename T, int kN>
 struct RingState {
     static constexpr int kSlots = RowRing<T, kN>::kSlots;
@@ -276,11 +264,7 @@ struct RingState {
         const unsigned all = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) mbar_arrive_expect_tx(&ring.bar[slot], all);
         __syncwarp();
-        if (n)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             smem_u32(ring.piece[slot][lane])),
-                         "l"(lo), "r"(n), "r"(smem_u32(&ring.bar[slot]))
-                         : "memory");
+        if (n) bulk_load(ring.piece[slot][lane], lo, n, &ring.bar[slot]);
     }
     // whether the slot's round is to be read from global memory; else waits for it
     __device__ __forceinline__ bool direct(int slot, bool& late) {

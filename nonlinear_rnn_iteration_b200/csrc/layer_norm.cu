@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "abi_util.cuh"
+#include "bulk.cuh"
 #include "common.cuh"
 #include "pararnn_b200.h"
 
@@ -55,11 +56,11 @@ struct BwdParams {
 // its rows.  U rows are read and reduced at a time: that keeps enough bytes in flight and
 // shares a block barrier between them.  Two reductions of a row in the forward pass
 // (the variance is taken about the mean), one of two sums in the backward pass.
-// Measured: 131072x1x1024 float32 192 us forward, 5.6 TB/s, and 279 us backward, 5.8 TB/s, bound by HBM;
-// 32768x3x2048 bfloat16 152 us, 5.3 TB/s, and 252 us, 4.8 TB/s, bound by the latency of the row
-// loads, for which registers are left; rows of 64, 32768x8x64 bfloat16, 22 us and 34 us, bound by
-// instructions (places kept as running sums and a reciprocal root of few instructions took
-// the forward from 27).  Reading a batch ahead gained nothing forward and spilled backward (49 us).
+// Measured: 131072x1x1024 float32 192 us forward, 5.6 TB/s, and 251 us backward, 6.4 TB/s, bound by HBM;
+// 32768x3x2048 bfloat16 152 us, 5.3 TB/s, bound by the latency of the row loads, for which
+// registers are left, and 249 us, 4.9 TB/s, bound by issue and the rows' barrier; rows of 64, 32768x8x64
+// bfloat16, 22 us and 34 us, bound by instructions (places kept as running sums and a reciprocal
+// root of few instructions took the forward from 27).
 template <typename T, int V, int K>
 constexpr int words_of = K * (V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1);
 constexpr int batch_of(int words) { return words >= 16 ? 1 : words >= 8 ? 2 : 4; }
@@ -189,13 +190,70 @@ struct Columns {
 };
 __device__ __forceinline__ float total(f2 x) { return x.x + x.y; }
 
+// The 16-byte accesses of a warp to a batch of rows, kN of them, brought ahead as pieces of 512
+// bytes by a bulk copy of one lane each, into the warp's own part of the shared memory: bytes are
+// in flight while the batch before is at work, without registers for them.
+template <int kN>
+struct Ring {
+    static constexpr int kBytes = kN * 512;
+    unsigned char* piece;
+    uint64_t* bar;
+    unsigned phase = 0;
+
+    __device__ __forceinline__ Ring(unsigned char* all, uint64_t* bars)
+        : piece(all + threadIdx.x / 32 * kBytes), bar(bars + threadIdx.x / 32) {
+        if (threadIdx.x % 32 == 0) {
+            mbar_init(bar, 1);
+            mbar_fence_init();
+        }
+        __syncwarp();
+    }
+    // where(i, src) gives the bytes of piece i and its place; 0 for none
+    template <class F>
+    __device__ __forceinline__ void fill(F where) {
+        const int lane = threadIdx.x % 32;
+        const void* src = nullptr;
+        const unsigned n = lane < kN ? where(lane, src) : 0u, all = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) mbar_arrive_expect_tx(bar, all);
+        __syncwarp();
+        if (n) bulk_load(piece + lane * 512, reinterpret_cast<uintptr_t>(src), n, bar);
+    }
+    __device__ __forceinline__ void wait(bool& late) {
+        wait_bar<false>(bar, phase, late);
+        phase ^= 1;
+    }
+    template <class V>
+    __device__ __forceinline__ V read(int i) const {
+        const uint4 q = *reinterpret_cast<const uint4*>(piece + i * 512 + threadIdx.x % 32 * 16);
+        V v;
+        v.r[0] = q.x, v.r[1] = q.y, v.r[2] = q.z, v.r[3] = q.w;
+        return v;
+    }
+};
+struct NoRing {
+    __device__ __forceinline__ NoRing(unsigned char*, uint64_t*) {}
+};
+// Where rows are brought ahead: with 16-byte accesses, and where a row has a warp at least (more
+// than 8 values a thread).  In the backward pass (131072x1x1024 float32 251 us, 279 without;
+// 32768x3x2048 bfloat16 249, 253), but not with 1024 threads, whose 64 registers spill (16384x1x16384
+// float32 1435 us, 1250 without).  In the forward only with 512 threads, one block to an SM
+// (16384x1x16384 float32 357, 454 without); more blocks hide the loads themselves, and the rings
+// take their shared memory (32768x3x2048 bfloat16 164, 152 without).
+template <typename T, int V, int K, int kThreads, bool kForward>
+constexpr bool kRing = V * sizeof(T) == 16 && V * K > 8 && (kForward ? kThreads == 512 : kThreads <= 512);
+// rows that a thread of the backward pass reads at a time
+template <typename T, int V, int K, int kThreads>
+constexpr int kBackRows = kThreads > 512 ? 1 : batch_of(words_of<T, V, K>);
+
 template <typename T, int V, int K, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_rows(const Params pr) {
     constexpr int U = batch_of(words_of<T, V, K>), E = K * V;
     // the weights in registers, or, for more values, in shared memory: [w, b][quads][threads of a row]
     constexpr bool kHold = E <= 16;
+    constexpr bool kAhead = kRing<T, V, K, kThreads, true>;
     __shared__ float buf[2][32][U];
-    extern __shared__ float4 held[];
+    __shared__ uint64_t bars[kAhead ? 32 : 1];
+    extern __shared__ __align__(16) float4 held[];
     follow_previous();
     Rows rows = rows_of(pr);
     const uint32_t M = (uint32_t)pr.M;
@@ -236,9 +294,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     }
     int64_t at0 = rows.row * N + c.j0;  // the thread's first value
     const int64_t dat = rows.drow * N;
+    bool late = false;
+    auto fill = [&](auto& ring) {
+        ring.fill([&](int i, const void*& src) {
+            const int u = i / K, j = (c.j0 & ~(32 * V - 1)) + i % K * c.dj;
+            src = static_cast<const T*>(pr.x) + rows.row * N + u * dat + j;
+            return rows.on && rows.m + u * rows.dm < M && j < N ? min(32 * V, N - j) * (unsigned)sizeof(T) : 0u;
+        });
+    };
+    std::conditional_t<kAhead, Ring<U * K>, NoRing> ring(
+        reinterpret_cast<unsigned char*>(held) + (kHold ? 0 : (size_t)quads * 2 * sizeof(float4)), bars);
+    if constexpr (kAhead) fill(ring);
     for (uint32_t it = 0; it < rows.steps; it += U) {
         Vec<T, V> v[U][K];
         float s[U], mean[U];
+        if constexpr (kAhead) ring.wait(late);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const T* x = static_cast<const T*>(pr.x) + at0 + u * dat;
@@ -246,9 +316,24 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 v[u][k] = Vec<T, V>{};
-                if (on && c.in(k)) v[u][k] = load<T, V>(x + k * c.dj);
+                if (on && c.in(k)) {
+                    if constexpr (kAhead)
+                        v[u][k] = ring.template read<Vec<T, V>>(u * K + k);
+                    else
+                        v[u][k] = load<T, V>(x + k * c.dj);
+                }
             }
         }
+        const uint32_t m = rows.m;
+        const int64_t row = rows.row, begin = at0;
+        rows.m += U * rows.dm;
+        rows.row += U * rows.drow;
+        at0 += U * dat;
+        if constexpr (kAhead)
+            if (it + U < rows.steps) {
+                __syncwarp();
+                fill(ring);
+            }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             f2 t{0.0f, 0.0f};
@@ -270,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!rows.on || rows.m + u * rows.dm >= M) continue;
+            if (!rows.on || m + u * rows.dm >= M) continue;
             const float rstd = rsqrtf(s[u] * inv + pr.eps);  // within 2 ulp
-            T* y = static_cast<T*>(pr.y) + at0 + u * dat;
+            T* y = static_cast<T*>(pr.y) + begin + u * dat;
             auto out = [&](int e, f2 we, f2 be) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd));
                 const f2 o = fma2(xh, we, be);
@@ -307,22 +392,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                         store<T, V>(y + k * c.dj, o);
                     }
             }
-            if (c.j0 == 0 && pr.mean) pr.mean[rows.row + u * rows.drow] = mean[u];
-            if (c.j0 == 0 && pr.rstd) pr.rstd[rows.row + u * rows.drow] = rstd;
+            if (c.j0 == 0 && pr.mean) pr.mean[row + u * rows.drow] = mean[u];
+            if (c.j0 == 0 && pr.rstd) pr.rstd[row + u * rows.drow] = rstd;
         }
-        rows.m += U * rows.dm;
-        rows.row += U * rows.drow;
-        at0 += U * dat;
     }
-    if (pr.status && total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
+    const unsigned bits = (total(chk) != total(chk) ? kStatusNonFinite : 0u) | (late ? kStatusTimeout : 0u);
+    if (pr.status && bits) atomicOr(pr.status, bits);
 }
 
 template <typename T, int V, int K, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_rows(const BwdParams pr) {
-    constexpr int U = kThreads > 512 ? 1 : batch_of(words_of<T, V, K>), E = K * V;
-    constexpr bool kHold = kThreads <= 512;
+    constexpr int U = kBackRows<T, V, K, kThreads>, E = K * V;
+    constexpr bool kHold = kThreads <= 512, kAhead = kRing<T, V, K, kThreads, false>;
     __shared__ float buf[2][32][2 * U];
-    extern __shared__ float2 sums[];  // [K * V][threads]
+    __shared__ uint64_t bars[kAhead ? 32 : 1];
+    extern __shared__ __align__(16) float2 sums[];  // [K * V][threads]; before that, the warps' rings
     follow_previous();
     Rows rows = rows_of(pr);
     const uint32_t M = (uint32_t)pr.M;
@@ -346,9 +430,35 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     if (kHold) params();
     int64_t at0 = rows.row * N + c.j0;  // the thread's first value
     const int64_t dat = rows.drow * N;
+    bool late = false;
+    auto fill = [&](auto& ring) {
+        ring.fill([&](int i, const void*& src) {
+            const int u = i / K / 2, j = (c.j0 & ~(32 * V - 1)) + i % K * c.dj;
+            src = static_cast<const T*>(i / K % 2 ? pr.dy : pr.x) + rows.row * N + u * dat + j;
+            return rows.on && rows.m + u * rows.dm < M && j < N ? min(32 * V, N - j) * (unsigned)sizeof(T) : 0u;
+        });
+    };
+    float mean[U], rstd[U];
+    auto stats = [&]() {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = rows.on && rows.m + u * rows.dm < M;
+            mean[u] = on ? pr.mean[rows.row + u * rows.drow] : 0.0f;
+            rstd[u] = on ? pr.rstd[rows.row + u * rows.drow] : 0.0f;
+        }
+    };
+    std::conditional_t<kAhead, Ring<2 * U * K>, NoRing> ring(reinterpret_cast<unsigned char*>(sums), bars);
+    if constexpr (kAhead) {
+        fill(ring);
+        stats();
+    }
     for (uint32_t it = 0; it < rows.steps; it += U) {
         Vec<T, V> v[U][K], g[U][K];
-        float mean[U], rstd[U], s[2 * U];
+        float s[2 * U];
+        if constexpr (kAhead)
+            ring.wait(late);
+        else
+            stats();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool on = rows.on && rows.m + u * rows.dm < M;
@@ -358,13 +468,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                 v[u][k] = Vec<T, V>{};
                 g[u][k] = Vec<T, V>{};
                 if (on && c.in(k)) {
-                    v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at + k * c.dj);
-                    g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + at + k * c.dj);
+                    if constexpr (kAhead) {
+                        v[u][k] = ring.template read<Vec<T, V>>(2 * u * K + k);
+                        g[u][k] = ring.template read<Vec<T, V>>((2 * u + 1) * K + k);
+                    } else {
+                        v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at + k * c.dj);
+                        g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + at + k * c.dj);
+                    }
                 }
             }
-            mean[u] = on ? pr.mean[rows.row + u * rows.drow] : 0.0f;
-            rstd[u] = on ? pr.rstd[rows.row + u * rows.drow] : 0.0f;
         }
+        const uint32_t m = rows.m;
+        const int64_t begin = at0;
+        rows.m += U * rows.dm;
+        rows.row += U * rows.drow;
+        at0 += U * dat;
+        if constexpr (kAhead)
+            if (it + U < rows.steps) {
+                __syncwarp();
+                fill(ring);
+            }
         if (!kHold) params();
         // rows past M hold zeros: they add nothing
 #pragma unroll
@@ -385,9 +508,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!rows.on || rows.m + u * rows.dm >= M) continue;
+            if (!rows.on || m + u * rows.dm >= M) continue;
             const f2 m1 = splat2(s[2 * u] * inv), m2 = splat2(-s[2 * u + 1] * inv);
-            T* o = static_cast<T*>(pr.dx) + at0 + u * dat;
+            T* o = static_cast<T*>(pr.dx) + begin + u * dat;
             auto out = [&](int e) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u]));
                 const f2 q = mul2(fma2(xh, m2, sub2(mul2(pair(g[u], e), w[e]), m1)), splat2(rstd[u]));
@@ -415,12 +538,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                     }
             }
         }
-        rows.m += U * rows.dm;
-        rows.row += U * rows.drow;
-        at0 += U * dat;
+        if constexpr (kAhead) stats();  // of the next batch
     }
-    if (total(chk) != total(chk)) atomicOr(pr.status, kStatusNonFinite);
+    const unsigned bits = (total(chk) != total(chk) ? kStatusNonFinite : 0u) | (late ? kStatusTimeout : 0u);
+    if (bits) atomicOr(pr.status, bits);
     if (!pr.part) return;
+    if constexpr (kAhead) __syncthreads();  // the sums lie where the rings were
     // the block's column sums: the groups of one parameter row in order
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -676,8 +799,11 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
     const int64_t blocks = slots_for(p, pr.M, sms, p.most == 256 ? 768 : p.most) * p.npc;
     pararnn_status s = PARARNN_EINVAL;
     with_shape<T, true>(p, [&](auto v, auto k, auto big) {
-        auto kern = forward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
-        const size_t smem = p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0;
+        constexpr int V = decltype(v)::value, K = decltype(k)::value, most = decltype(big)::value;
+        auto kern = forward_rows<T, V, K, most>;
+        constexpr int words = words_of<T, V, K>;
+        const size_t smem = (p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0) +
+                            (kRing<T, V, K, most, true> ? (size_t)p.threads * words * batch_of(words) * 4 : 0);
         if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         s = abi::launch(who, kern, dim3((unsigned)blocks), p.threads, smem, st, 1, pr);
     });
@@ -710,9 +836,12 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
         parts = slots_for(p, pr.M, sms, p.most == 256 ? 512 : p.most);
         if (sums) parts = std::min<int64_t>(parts, max_parts(pr.M, C));
         with_shape<T, false>(p, [&](auto v, auto k, auto big) {
-            constexpr int each = decltype(v)::value * decltype(k)::value;
-            auto kern = backward_rows<T, decltype(v)::value, decltype(k)::value, decltype(big)::value>;
-            const size_t smem = sums ? (size_t)each * p.threads * sizeof(float2) : 0;
+            constexpr int V = decltype(v)::value, K = decltype(k)::value, most = decltype(big)::value;
+            auto kern = backward_rows<T, V, K, most>;
+            const size_t ring = kRing<T, V, K, most, false>
+                                    ? (size_t)p.threads * words_of<T, V, K> * kBackRows<T, V, K, most> * 8
+                                    : 0;
+            const size_t smem = std::max(sums ? (size_t)V * K * p.threads * sizeof(float2) : 0, ring);
             if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             s = abi::launch(who, kern, dim3((unsigned)(parts * p.npc)), p.threads, smem, st, 1, pr);
         });

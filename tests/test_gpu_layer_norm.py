@@ -52,6 +52,38 @@ def test_forward_and_backward(shape, dtype):
     assert dw.shape == db.shape == (P, N)
 
 
+# several batches of rows for each thread, at each count of threads to a row; the last piece of a row short
+@pytest.mark.parametrize("M,P,N,dtype", [(1500, 3, 2048, "bf16"), (1111, 2, 1000, "bf16"), (2500, 1, 520, "f32"),
+                                         (900, 5, 296, "bf16"), (600, 1, 8192, "f32"), (700, 1, 12344, "f32"),
+                                         (700, 1, 9000, "bf16")])
+def test_many_rows_a_thread_and_in_place(M, P, N, dtype):
+    x, w, b, dy = make(M, P, N, dtype, M)
+    n = [f64(t) for t in (x, w, b, dy)]
+    y, mean, rstd = binding.layer_norm_forward(x, w, b, want_stats=True)
+    dx, dw, db = binding.layer_norm_backward(x, dy, mean, rstd, w)
+    ey, em, er, edx, ew, eb = ref.norm_bounds(n[0], n[1], n[2], 1e-5, dtype, n[3])
+    for got, want, bound, name in zip((y, mean, rstd), ref.norm(n[0], n[1], n[2], 1e-5), (ey, em, er),
+                                      ("y", "mean", "rstd")):
+        within(got, want, bound, name)
+    for got, want, bound, name in zip((dx, dw, db), ref.norm_backward(n[0], n[3], n[1], 1e-5), (edx, ew, eb),
+                                      ("dx", "dweight", "dbias")):
+        within(got, want, bound, name)
+    # dx over dy and over x, and y over x: the same bits
+    code = binding.BF16 if dtype == "bf16" else binding.F32
+    ws = torch.empty(binding.pararnn_layer_norm_workspace_bytes(M, P, N), dtype=torch.uint8, device="cuda")
+    for over in ("dy", "x"):
+        xs, gs = x.clone(), dy.clone()
+        to = gs if over == "dy" else xs
+        dw2, db2 = torch.empty_like(dw), torch.empty_like(db)
+        assert binding.pararnn_layer_norm_backward(M, P, N, code, xs, w, mean, rstd, gs, to, dw2, db2, ws, ws.numel(),
+                                                   None) == binding.OK
+        assert torch.equal(to, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+    xs = x.clone()
+    assert binding.pararnn_layer_norm_forward(M, P, N, code, xs, w, b, 1e-5, xs, None, None, None, 0,
+                                              None) == binding.OK
+    assert torch.equal(xs, y)
+
+
 def test_shapes_of_the_parameters():
     x = torch.randn(2, 5, 3, 16, device="cuda")
     want, _, _ = ref.norm(f64(x).reshape(30, 1, 16), None, None, 1e-5)

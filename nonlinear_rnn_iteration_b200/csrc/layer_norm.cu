@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     constexpr bool kHold = kThreads <= 512, kAhead = kRing<T, V, K, kThreads, false>;
     __shared__ float buf[2][32][2 * U];
     __shared__ uint64_t bars[kAhead ? 32 : 1];
-    extern __shared__ __align__(16) float2 sums[];  // [K * V][threads]; before that, the warps' rings
+    extern __shared__ __align__(16) float4 sums[];  // [K * V / 2][threads]; before that, the warps' rings
     follow_previous();
     Rows rows = rows_of(pr);
     const uint32_t M = (uint32_t)pr.M;
@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     const int N = c.N;
     const float inv = 1.0f / (float)N;
     int turn = 0;
-    f2 w[E / 2], dw[E / 2], db[E / 2], chk{0.0f, 0.0f};
+    // with 1024 threads, of 64 registers, the column sums stay in shared memory (16384x1x16384 float32
+    // 1112 us, in spilled registers 1287)
+    f2 w[E / 2], dw[kHold ? E / 2 : 1], db[kHold ? E / 2 : 1], chk{0.0f, 0.0f};
     auto params = [&]() {
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
@@ -425,9 +427,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
             }
         }
     };
+    if constexpr (kHold) {
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = splat2(0.0f);
-    if (kHold) params();
+        for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = splat2(0.0f);
+        params();
+    } else if (pr.part) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) sums[e * kThreads + threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     int64_t at0 = rows.row * N + c.j0;  // the thread's first value
     const int64_t dat = rows.drow * N;
     bool late = false;
@@ -499,8 +506,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                 const f2 dy = pair(g[u], e), d = mul2(dy, w[e]);
                 t1 = add2(t1, d);
                 t2 = fma2(d, xh, t2);
-                db[e] = add2(db[e], dy);
-                dw[e] = fma2(dy, xh, dw[e]);
+                if constexpr (kHold) {
+                    db[e] = add2(db[e], dy);
+                    dw[e] = fma2(dy, xh, dw[e]);
+                } else if (pr.part) {
+                    float4& q = sums[e * kThreads + threadIdx.x];
+                    const f2 tw = fma2(dy, xh, f2{q.x, q.y}), tb = add2(f2{q.z, q.w}, dy);
+                    q = make_float4(tw.x, tw.y, tb.x, tb.y);
+                }
             });
             s[2 * u] = total(t1);
             s[2 * u + 1] = total(t2);
@@ -545,26 +558,24 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     if (!pr.part) return;
     if constexpr (kAhead) __syncthreads();  // the sums lie where the rings were
     // the block's column sums: the groups of one parameter row in order
+    if constexpr (kHold)
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        sums[e * blockDim.x + threadIdx.x] =
-            e & 1 ? make_float2(dw[e / 2].y, db[e / 2].y) : make_float2(dw[e / 2].x, db[e / 2].x);
+        for (int e = 0; e < E / 2; ++e)
+            sums[e * blockDim.x + threadIdx.x] = make_float4(dw[e].x, dw[e].y, db[e].x, db[e].y);
     __syncthreads();
     const int g0 = threadIdx.x / pr.tpr;
     if (g0 < pr.pb && rows.p < pr.P) {
         float* to = pr.part + (int64_t)(blockIdx.x / pr.npc) * 2 * pr.P * N + rows.p * N;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = c.of(e);
-            float2 t = make_float2(0.0f, 0.0f);
+        for (int e = 0; e < E / 2; ++e) {
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int q = 0; q < pr.gpp; ++q) {
-                const float2 u = sums[e * blockDim.x + threadIdx.x + q * pr.pb * pr.tpr];
-                t.x += u.x, t.y += u.y;
+                const float4 u = sums[e * blockDim.x + threadIdx.x + q * pr.pb * pr.tpr];
+                t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
             }
-            if (j < N) {
-                to[j] = t.x;
-                to[pr.P * N + j] = t.y;
-            }
+            const int j = c.of(2 * e), j1 = c.of(2 * e + 1);
+            if (j < N) to[j] = t.x, to[pr.P * N + j] = t.z;
+            if (j1 < N) to[j1] = t.y, to[pr.P * N + j1] = t.w;
         }
     }
 }
@@ -717,15 +728,17 @@ int pow2_at_least(int64_t n) {
 
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
 // of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16: 152 us with
-// 64 values and a warp per row, 270 with 8 and a block); the backward pass, which holds two
-// column sums for each value, has 8, or 16 past 256 columns (the same rows: 254 us with 16, 289 with 8).
-// With few rows the smaller count leaves more threads to each of them.  A row of 256 bytes or
-// more needs no neighbours: the block's rows then share one parameter row.
+// 64 values and a warp per row, 270 with 8 and a block); past 8192 columns, where the weights in
+// shared memory leave one block to an SM, 32 and so 512 threads (16384x1x16384 bfloat16 272 us,
+// 437 with 64 and 256 threads).  With few rows the smaller count leaves more threads to each of
+// them.  The backward pass, which holds two column sums for each value, has 8, or 16 past 256
+// columns (32768x3x2048 bfloat16: 249 us with 16, 289 with 8).  A row of 256 bytes or more needs no
+// neighbours: the block's rows then share one parameter row.
 Plan plan_of(int64_t M, int64_t P, int64_t N, int esz, bool by16, bool by4, bool forward, int sms) {
     Plan p{};
     p.vec = by16 ? 16 / esz : (esz == 2 && by4) ? 2 : 1;
     if (N > 16384) return Plan{};
-    const int most = !forward ? 16 : esz == 2 && p.vec > 1 ? 64 : 32;
+    const int most = !forward ? 16 : esz == 2 && p.vec > 1 && N <= 8192 ? 64 : 32;
     p.each = 8;
     if (forward) {
         while (p.each < most && p.each * 32 < N && (double)M * P * N >= 768.0 * sms * p.each) p.each *= 2;

@@ -56,11 +56,15 @@ struct BwdParams {
 // its rows.  U rows are read and reduced at a time: that keeps enough bytes in flight and
 // shares a block barrier between them.  Two reductions of a row in the forward pass
 // (the variance is taken about the mean), one of two sums in the backward pass.
-// Measured: 131072x1x1024 float32 192 us forward, 5.6 TB/s, and 251 us backward, 6.4 TB/s, bound by HBM;
+// Batches in which every thread of the block has all its values take a copy of the code without
+// conditions (100000x1x256 bfloat16 27 and 43 us, 29 and 45 without), where its registers allow that:
+// with 64 values a thread forward (32768x3x2048 163 us, 152 without the copy) and 16 backward
+// (283, 248 without) it spills.
+// Measured: 131072x1x1024 float32 188 us forward, 5.7 TB/s, and 250 us backward, 6.4 TB/s, bound by HBM;
 // 32768x3x2048 bfloat16 152 us, 5.3 TB/s, bound by the latency of the row loads, for which
 // registers are left, and 249 us, 4.9 TB/s, bound by issue and the rows' barrier; rows of 64, 32768x8x64
-// bfloat16, 22 us and 34 us, bound by instructions (places kept as running sums and a reciprocal
-// root of few instructions took the forward from 27).
+// bfloat16, 21 us and 33 us, bound by instructions (places kept as running sums and a reciprocal
+// root of few instructions took the forward from 27 to 22).
 template <typename T, int V, int K>
 constexpr int words_of = K * (V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1);
 constexpr int batch_of(int words) { return words >= 16 ? 1 : words >= 8 ? 2 : 4; }
@@ -138,10 +142,11 @@ __device__ __forceinline__ void row_sums(float (&a)[n], int tpr, float (*buf)[32
 struct Rows {
     int64_t p, row, drow;  // the first row, and the way to the next
     uint32_t m, dm, steps;  // steps: of the whole block, the most rows that one of its groups has
+    uint32_t full;          // the first steps in which every thread of the block has `each` values
     bool on;
 };
 template <class P>
-__device__ __forceinline__ Rows rows_of(const P& pr) {
+__device__ __forceinline__ Rows rows_of(const P& pr, int each) {
     const int g = threadIdx.x / pr.tpr;
     const int64_t range = blockIdx.x % pr.npc, slot = blockIdx.x / pr.npc, slots = gridDim.x / pr.npc;
     Rows r;
@@ -152,6 +157,9 @@ __device__ __forceinline__ Rows rows_of(const P& pr) {
     r.drow = (int64_t)r.dm * pr.P;
     r.on = g < pr.pb * pr.gpp && r.p < pr.P;
     r.steps = (uint32_t)((pr.M - slot * pr.gpp + r.dm - 1) / r.dm);
+    const int64_t last = pr.M - (slot * pr.gpp + pr.gpp - 1);
+    const bool all = pr.pb * pr.gpp * pr.tpr == (int)blockDim.x && (range + 1) * pr.pb <= pr.P && pr.N == pr.tpr * each;
+    r.full = all && last > 0 ? (uint32_t)((last + r.dm - 1) / r.dm) : 0u;
     return r;
 }
 
@@ -163,14 +171,14 @@ __device__ __forceinline__ f2 pair(const Vec<T, V> (&v)[K], int e) {
     return f2{value<T, V>(v[2 * e / V], 2 * e % V), value<T, V>(v[2 * e / V], 2 * e % V + 1)};
 }
 // columns of a thread: which of its values lie in the row
-template <int V, int K>
+template <int V, int K, bool kFull = false>
 struct Columns {
     int j0, dj, N;
     __device__ __forceinline__ int of(int e) const { return j0 + e / V * dj + e % V; }
-    __device__ __forceinline__ bool in(int k) const { return j0 + k * dj < N; }
+    __device__ __forceinline__ bool in(int k) const { return kFull || j0 + k * dj < N; }
     // a pair with zeros in place of the values past the row, where V is 1
     __device__ __forceinline__ f2 mask(f2 x, int e) const {
-        if constexpr (V > 1) return x;
+        if constexpr (V > 1 || kFull) return x;
         return f2{in(2 * e) ? x.x : 0.0f, in(2 * e + 1) ? x.y : 0.0f};
     }
     // f(e) for the pairs that lie in the row, at least in part
@@ -237,7 +245,7 @@ struct NoRing {
 // than 8 values a thread).  In the backward pass (131072x1x1024 float32 251 us, 279 without;
 // 32768x3x2048 bfloat16 249, 253), but not with 1024 threads, whose 64 registers spill (16384x1x16384
 // float32 1435 us, 1250 without).  In the forward only with 512 threads, one block to an SM
-// (16384x1x16384 float32 357, 454 without); more blocks hide the loads themselves, and the rings
+// (16384x1x16384 float32 377, 454 without); more blocks hide the loads themselves, and the rings
 // take their shared memory (32768x3x2048 bfloat16 164, 152 without).
 template <typename T, int V, int K, int kThreads, bool kForward>
 constexpr bool kRing = V * sizeof(T) == 16 && V * K > 8 && (kForward ? kThreads == 512 : kThreads <= 512);
@@ -255,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     __shared__ uint64_t bars[kAhead ? 32 : 1];
     extern __shared__ __align__(16) float4 held[];
     follow_previous();
-    Rows rows = rows_of(pr);
+    Rows rows = rows_of(pr, E);
     const uint32_t M = (uint32_t)pr.M;
-    const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
-    const int N = c.N;
+    const Columns<V, K> c0{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
+    const int N = c0.N;
     const float inv = 1.0f / (float)N;
     int turn = 0;
     f2 chk{0.0f, 0.0f}, w[kHold ? E / 2 : 1], b[kHold ? E / 2 : 1];
@@ -266,16 +274,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         f2 o{none, none};
         if (from) {
             if constexpr (V == 1) {
-                if (c.of(2 * e) < N) o.x = from[rows.p * N + c.of(2 * e)];
-                if (c.of(2 * e + 1) < N) o.y = from[rows.p * N + c.of(2 * e + 1)];
-            } else if (c.of(2 * e) < N) {
-                const float* q = from + rows.p * N + c.of(2 * e);
+                if (c0.of(2 * e) < N) o.x = from[rows.p * N + c0.of(2 * e)];
+                if (c0.of(2 * e + 1) < N) o.y = from[rows.p * N + c0.of(2 * e + 1)];
+            } else if (c0.of(2 * e) < N) {
+                const float* q = from + rows.p * N + c0.of(2 * e);
                 o = f2{q[0], q[1]};
             }
         }
         return o;
     };
-    const int quads = pr.tpr * (E / 4), at = c.j0 / V;
+    const int quads = pr.tpr * (E / 4), at = c0.j0 / V;
     if constexpr (kHold) {
         if (rows.on)
 #pragma unroll
@@ -292,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
             }
         __syncthreads();
     }
-    int64_t at0 = rows.row * N + c.j0;  // the thread's first value
+    int64_t at0 = rows.row * N + c0.j0;  // the thread's first value
     const int64_t dat = rows.drow * N;
     bool late = false;
     auto fill = [&](auto& ring) {
         ring.fill([&](int i, const void*& src) {
-            const int u = i / K, j = (c.j0 & ~(32 * V - 1)) + i % K * c.dj;
+            const int u = i / K, j = (c0.j0 & ~(32 * V - 1)) + i % K * c0.dj;
             src = static_cast<const T*>(pr.x) + rows.row * N + u * dat + j;
             return rows.on && rows.m + u * rows.dm < M && j < N ? min(32 * V, N - j) * (unsigned)sizeof(T) : 0u;
         });
@@ -305,14 +313,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     std::conditional_t<kAhead, Ring<U * K>, NoRing> ring(
         reinterpret_cast<unsigned char*>(held) + (kHold ? 0 : (size_t)quads * 2 * sizeof(float4)), bars);
     if constexpr (kAhead) fill(ring);
-    for (uint32_t it = 0; it < rows.steps; it += U) {
+    auto batch = [&](uint32_t it, auto full) {
+        constexpr bool kFull = decltype(full)::value;
+        const Columns<V, K, kFull> c{c0.j0, c0.dj, N};
         Vec<T, V> v[U][K];
         float s[U], mean[U];
         if constexpr (kAhead) ring.wait(late);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const T* x = static_cast<const T*>(pr.x) + at0 + u * dat;
-            const bool on = rows.on && rows.m + u * rows.dm < M;
+            const bool on = kFull || (rows.on && rows.m + u * rows.dm < M);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 v[u][k] = Vec<T, V>{};
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
                     if constexpr (kAhead)
                         v[u][k] = ring.template read<Vec<T, V>>(u * K + k);
                     else
-                        v[u][k] = load<T, V>(x + k * c.dj);
+                        v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at0 + u * dat + k * c.dj);
                 }
             }
         }
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!rows.on || m + u * rows.dm >= M) continue;
+            if (!kFull && (!rows.on || m + u * rows.dm >= M)) continue;
             const float rstd = rsqrtf(s[u] * inv + pr.eps);  // within 2 ulp
             T* y = static_cast<T*>(pr.y) + begin + u * dat;
             auto out = [&](int e, f2 we, f2 be) {
@@ -395,6 +404,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
             if (c.j0 == 0 && pr.mean) pr.mean[row + u * rows.drow] = mean[u];
             if (c.j0 == 0 && pr.rstd) pr.rstd[row + u * rows.drow] = rstd;
         }
+    };
+    for (uint32_t it = 0; it < rows.steps; it += U) {
+        if constexpr (E <= 32)
+            it + U <= rows.full ? batch(it, std::true_type{}) : batch(it, std::false_type{});
+        else
+            batch(it, std::false_type{});
     }
     const unsigned bits = (total(chk) != total(chk) ? kStatusNonFinite : 0u) | (late ? kStatusTimeout : 0u);
     if (pr.status && bits) atomicOr(pr.status, bits);
@@ -408,10 +423,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     __shared__ uint64_t bars[kAhead ? 32 : 1];
     extern __shared__ __align__(16) float4 sums[];  // [K * V / 2][threads]; before that, the warps' rings
     follow_previous();
-    Rows rows = rows_of(pr);
+    Rows rows = rows_of(pr, E);
     const uint32_t M = (uint32_t)pr.M;
-    const Columns<V, K> c{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
-    const int N = c.N;
+    const Columns<V, K> c0{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
+    const int N = c0.N;
     const float inv = 1.0f / (float)N;
     int turn = 0;
     // with 1024 threads, of 64 registers, the column sums stay in shared memory (16384x1x16384 float32
@@ -422,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
         for (int e = 0; e < E / 2; ++e) {
             w[e] = splat2(1.0f);
             if (pr.w && rows.on) {
-                if (c.of(2 * e) < N) w[e].x = pr.w[rows.p * N + c.of(2 * e)];
-                if (c.of(2 * e + 1) < N) w[e].y = pr.w[rows.p * N + c.of(2 * e + 1)];
+                if (c0.of(2 * e) < N) w[e].x = pr.w[rows.p * N + c0.of(2 * e)];
+                if (c0.of(2 * e + 1) < N) w[e].y = pr.w[rows.p * N + c0.of(2 * e + 1)];
             }
         }
     };
@@ -435,12 +450,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) sums[e * kThreads + threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    int64_t at0 = rows.row * N + c.j0;  // the thread's first value
+    int64_t at0 = rows.row * N + c0.j0;  // the thread's first value
     const int64_t dat = rows.drow * N;
     bool late = false;
     auto fill = [&](auto& ring) {
         ring.fill([&](int i, const void*& src) {
-            const int u = i / K / 2, j = (c.j0 & ~(32 * V - 1)) + i % K * c.dj;
+            const int u = i / K / 2, j = (c0.j0 & ~(32 * V - 1)) + i % K * c0.dj;
             src = static_cast<const T*>(i / K % 2 ? pr.dy : pr.x) + rows.row * N + u * dat + j;
             return rows.on && rows.m + u * rows.dm < M && j < N ? min(32 * V, N - j) * (unsigned)sizeof(T) : 0u;
         });
@@ -459,7 +474,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
         fill(ring);
         stats();
     }
-    for (uint32_t it = 0; it < rows.steps; it += U) {
+    auto batch = [&](uint32_t it, auto full) {
+        constexpr bool kFull = decltype(full)::value;
+        const Columns<V, K, kFull> c{c0.j0, c0.dj, N};
         Vec<T, V> v[U][K], g[U][K];
         float s[2 * U];
         if constexpr (kAhead)
@@ -468,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
             stats();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool on = rows.on && rows.m + u * rows.dm < M;
-            const int64_t at = at0 + u * dat;
+            const bool on = kFull || (rows.on && rows.m + u * rows.dm < M);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 v[u][k] = Vec<T, V>{};
@@ -479,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                         v[u][k] = ring.template read<Vec<T, V>>(2 * u * K + k);
                         g[u][k] = ring.template read<Vec<T, V>>((2 * u + 1) * K + k);
                     } else {
-                        v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at + k * c.dj);
-                        g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + at + k * c.dj);
+                        v[u][k] = load<T, V>(static_cast<const T*>(pr.x) + at0 + u * dat + k * c.dj);
+                        g[u][k] = load<T, V>(static_cast<const T*>(pr.dy) + at0 + u * dat + k * c.dj);
                     }
                 }
             }
@@ -521,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!rows.on || m + u * rows.dm >= M) continue;
+            if (!kFull && (!rows.on || m + u * rows.dm >= M)) continue;
             const f2 m1 = splat2(s[2 * u] * inv), m2 = splat2(-s[2 * u + 1] * inv);
             T* o = static_cast<T*>(pr.dx) + begin + u * dat;
             auto out = [&](int e) {
@@ -552,6 +568,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
             }
         }
         if constexpr (kAhead) stats();  // of the next batch
+    };
+    for (uint32_t it = 0; it < rows.steps; it += U) {
+        if constexpr (E <= 8)
+            it + U <= rows.full ? batch(it, std::true_type{}) : batch(it, std::false_type{});
+        else
+            batch(it, std::false_type{});
     }
     const unsigned bits = (total(chk) != total(chk) ? kStatusNonFinite : 0u) | (late ? kStatusTimeout : 0u);
     if (bits) atomicOr(pr.status, bits);
@@ -573,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
                 const float4 u = sums[e * blockDim.x + threadIdx.x + q * pr.pb * pr.tpr];
                 t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
             }
-            const int j = c.of(2 * e), j1 = c.of(2 * e + 1);
+            const int j = c0.of(2 * e), j1 = c0.of(2 * e + 1);
             if (j < N) to[j] = t.x, to[pr.P * N + j] = t.z;
             if (j1 < N) to[j1] = t.y, to[pr.P * N + j1] = t.w;
         }

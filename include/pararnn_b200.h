@@ -544,10 +544,13 @@ pararnn_status pararnn_gated_scan_step(int64_t N, int64_t D, pararnn_dtype dtype
  * counterpart: it is the normalisation around a recurrent layer.)
  *   x, y          (M, P, N)  dtype (float32 or bfloat16); y may be x's buffer
  *   weight, bias  (P, N)     float32, or NULL for ones, zeros
- *   eps           finite, >= 0.  A constant row with eps = 0 gives NaN (0 times
- *                 Inf)
+ *   eps           finite, >= 0.  A constant row has no spread, and with eps = 0
+ *                 gives NaN (0 times Inf), where float32 holds its sums, of N and of
+ *                 fewer of its values, exactly, as it does for bfloat16 values and N
+ *                 up to 65536; elsewhere what their rounding leaves is its spread
  *   mean, rstd    (M, P)     float32, written; or NULL
- * P and N are at least 1; M*P and P*N must be below 2^31.  Sums are float32.
+ * P and N are at least 1; M*P and P*N must be below 2^31.  Sums are float32: a
+ * row whose squares about the mean add up past its range has rstd 0.
  * Workspace (NULL or 256 bytes) and errors as for pararnn_gated_scan_forward. */
 pararnn_status pararnn_layer_norm_forward(int64_t M, int64_t P, int64_t N, pararnn_dtype dtype, const void* x,
                                           const float* weight, const float* bias, float eps, void* y, float* mean,

@@ -198,6 +198,16 @@ struct Columns {
 };
 __device__ __forceinline__ float total(f2 x) { return x.x + x.y; }
 
+// s / n from inv = 1 / n, rounded: the product is up to 1.5 steps off (of a constant row's mean, with n = 1000, for
+// most values), and what it leaves of s, which one fused multiply-add gives exactly, corrects it (P. W. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", IBM J. Res. Dev. 34 (1990)): where s is a
+// multiple of n the mean is exact, so that a constant row, whatever its size, has no spread.  A division
+// in its place is a call, around which most of these kernels spill.
+__device__ __forceinline__ float mean_of(float s, float n, float inv) {
+    const float q = s * inv;
+    return __fmaf_rn(__fmaf_rn(-q, n, s), inv, q);
+}
+
 // The 16-byte accesses of a warp to a batch of rows, kN of them, brought ahead as pieces of 512
 // bytes by a bulk copy of one lane each, into the warp's own part of the shared memory: bytes are
 // in flight while the batch before is at work, without registers for them.
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
     const uint32_t M = (uint32_t)pr.M;
     const Columns<V, K> c0{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c0.N;
-    const float inv = 1.0f / (float)N;
+    const float n = (float)N, inv = 1.0f / n;
     int turn = 0;
     f2 chk{0.0f, 0.0f}, w[kHold ? E / 2 : 1], b[kHold ? E / 2 : 1];
     auto weight = [&](const float* from, int e, float none) {
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         row_sums(s, pr.tpr, buf, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mean[u] = s[u] * inv;
+            mean[u] = mean_of(s[u], n, inv);
             f2 t{0.0f, 0.0f};
             c.each([&](int e) {
                 const f2 d = c.mask(sub2(pair(v[u], e), splat2(mean[u])), e);
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     const uint32_t M = (uint32_t)pr.M;
     const Columns<V, K> c0{(int)(threadIdx.x % pr.tpr) * V, pr.tpr * V, (int)pr.N};
     const int N = c0.N;
-    const float inv = 1.0f / (float)N;
+    const float n = (float)N, inv = 1.0f / n;
     int turn = 0;
     // with 1024 threads, of 64 registers, the column sums stay in shared memory (16384x1x16384 float32
     // 1112 us, in spilled registers 1287)
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!kFull && (!rows.on || m + u * rows.dm >= M)) continue;
-            const f2 m1 = splat2(s[2 * u] * inv), m2 = splat2(-s[2 * u + 1] * inv);
+            const f2 m1 = splat2(mean_of(s[2 * u], n, inv)), m2 = splat2(-s[2 * u + 1] * inv);
             T* o = static_cast<T*>(pr.dx) + begin + u * dat;
             auto out = [&](int e) {
                 const f2 xh = mul2(sub2(pair(v[u], e), splat2(mean[u])), splat2(rstd[u]));

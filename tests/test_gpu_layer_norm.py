@@ -247,3 +247,37 @@ def test_together_as_a_layer():
         h = ref.forward(pn[:, None], f64(lam), 8.0, h)[1]
         assert np.abs(f64(yt) - h).max() <= tol * np.abs(h).max()
     assert torch.equal(cache[slots.long()], yt)
+
+
+# N whose float32 reciprocal times an exact sum misses the mean (56 to 1000), others, and each count of threads to a row
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [14, 56, 120, 1000, 3000, 6040, 12000])
+def test_means_are_quotients(N, dtype):
+    """Values of 8 bits: every partial sum of up to 2^14 of them is exact in float32, so a mean that is the rounded
+    quotient is the value itself, and what is left of a constant row, forward and backward, is nothing."""
+    value = torch.tensor([1.0, 101.0, -724.0, 15424.0, 9984.0], device="cuda")
+    M = 5 * max(1, 800_000 // N)
+    x = value.repeat(M // 5).view(M, 1, 1).expand(M, 1, N).to(TYPES[dtype]).contiguous()
+    b = torch.randn(1, N, device="cuda")
+    signs = torch.tensor([1.0, -1.0], device="cuda").repeat(M * N // 2).view(M, 1, N).to(TYPES[dtype])
+    for off in (0, 1):  # with 16-byte accesses where N allows them, and of single values
+        at = lambda t: torch.cat([t.new_zeros(off), t.reshape(-1)])[off:].view(t.shape)  # noqa: E731
+        y, m, r = binding.layer_norm_forward(at(x), None, b, want_stats=True)
+        assert torch.equal(m.view(-1), x[:, 0, 0].float())
+        assert torch.equal(y, b.to(y.dtype).expand(M, 1, N))
+        y, _, _ = binding.layer_norm_forward(at(x), None, b, eps=0.0, sync_status=False)
+        assert torch.isnan(y).all()  # 0 times Inf
+        # rows of 1 and -1 in turn: their xh add up to zero, whatever the order, as each has its opposite beside
+        # it; a constant dL/dy less its own mean is then all of dL/dx
+        _, m, r = binding.layer_norm_forward(at(signs), want_stats=True)
+        assert (m == 0).all()
+        dx, _, _ = binding.layer_norm_backward(at(signs), at(x), m, r)
+        assert (dx == 0).all()
+
+
+def test_mean_of_an_exact_sum_is_rounded_once():
+    # multiples of 1/2 next to 4096: 14 bits, and 9 more for the sum of 500 of them, so the sum is exact
+    x = torch.randint(-8, 9, (400, 1, 500), device="cuda").float() / 2 + 4096.0
+    _, m, _ = binding.layer_norm_forward(x, want_stats=True)
+    want = f64(x).mean(-1)
+    within(m, want, ref.U * np.abs(want), "mean")

@@ -478,7 +478,9 @@ pararnn_status pararnn_head_gru_unroll(int64_t B, int64_t T, int64_t D, int n_he
  * workspace    NULL, and device-detected conditions are not recorded; or at least
  *              256 bytes, 16-byte aligned, any contents, for
  *              pararnn_status_sync(), which reports a NaN or Inf in H or h_last as
- *              PARARNN_ENONFINITE.  With pararnn_gated_scan_workspace_bytes(B, T, D)
+ *              PARARNN_ENONFINITE.  (Here and below values are looked at in float32:
+ *              a finite one that only its rounding to bfloat16 makes Inf, above
+ *              3.39e38, is not reported.)  With pararnn_gated_scan_workspace_bytes(B, T, D)
  *              bytes a long sequence of few channels (B * ceil(D / 64) <= 16) is cut
  *              into ranges that run at the same time, which joins the scan in
  *              another order: the same result up to rounding.
@@ -508,8 +510,8 @@ pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, parar
  *   workspace   >= pararnn_gated_scan_workspace_bytes(B, T, D) bytes, 16-byte
  *               aligned, any contents; calls that overlap on the GPU, replays of
  *               captured ones among them, need workspaces of their own
- * Errors as for the forward; a NaN or Inf in dL_dpx is recorded for
- * pararnn_status_sync(). */
+ * Errors as for the forward; a NaN or Inf in dL_dpx or in the sum of w is recorded
+ * for pararnn_status_sync(). */
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D);
 pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,
                                            const float* lambda, float decay, const uint8_t* reset,

@@ -725,6 +725,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
     };
     unsigned mark = kCuts ? marks_of(0) : 0u;
     bool late = false;
+    // chk becomes NaN with a dL/dp_i that is not finite, and so with such a dL/dx, a factor of it
     f2 sum{0.0f, 0.0f}, chk{0.0f, 0.0f};
     Elem whole{splat2(1.0f), splat2(0.0f)};  // kSum: of the range, in warp 0
 
@@ -931,7 +932,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
             for (int j = 0; j < R; ++j) {
                 grads2(y[j], sub2(splat2(1.0f), m[j]), m[j], l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                 part = add2(part, w);
-                chk = fma2(dx, splat2(0.0f), chk);
+                chk = fma2(dpi, splat2(0.0f), chk);
                 put(j, o, dpr, dpi, dx);
                 o += 3 * (int64_t)D;
             }
@@ -951,7 +952,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
                     decay2<true>(y[j], a, mm);
                     grads2(y[j], a, mm, l[j], at_ix(j, 0), at_ix(j, 1), kinv, h, dpr, dpi, dx, w);
                     part = add2(part, w);
-                    chk = fma2(dx, splat2(0.0f), chk);
+                    chk = fma2(dpi, splat2(0.0f), chk);
                     put(j, o, dpr, dpi, dx);
                 }
                 o += 3 * (int64_t)D;

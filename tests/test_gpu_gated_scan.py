@@ -406,3 +406,20 @@ def test_offsets_past_32_bits():
     gp, _, _ = ref.backward(n[0], n[1], DECAY, f64(dH[:, :, ch]))
     ep, _, _ = ref.backward_bound(n[0], n[1], DECAY, f64(dH[:, :, ch]), "bf16")
     within(dpx[:, :, :, ch], gp, ep, "dpx")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 33])
+def test_gradient_of_the_input_gate_that_overflows_is_reported(dtype, D):
+    """dL/dp_i = l b i x (1 - i) = Inf while dL/dx = l b i and dL/dp_r (a^2 is 4e-18) are finite"""
+    px = torch.zeros(1, 1, 3, D, device="cuda")
+    px[:, :, 0], px[:, :, 2] = 20.0, 1e20
+    lam = torch.full((D,), 2.4, device="cuda")  # y = 8 softplus(2.4) = 20
+    px = px.to(TYPES[dtype])
+    dH = torch.full((1, 1, D), 1e25, device="cuda").to(TYPES[dtype])
+    _, _, ck = binding.gated_scan_forward(px, lam, DECAY, want_grad=True)
+    dpx, _, _ = binding.gated_scan_backward(px, lam, ck, dH, DECAY, sync_status=False)
+    assert torch.isinf(dpx[:, :, 1]).all() and torch.isfinite(dpx[:, :, [0, 2]]).all()
+    with pytest.raises(binding.PararnnError) as e:
+        binding.gated_scan_backward(px, lam, ck, dH, DECAY)
+    assert e.value.status == binding.ENONFINITE

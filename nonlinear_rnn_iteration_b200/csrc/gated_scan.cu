@@ -314,17 +314,34 @@ __device__ __forceinline__ void decay2(f2 y, f2& a, f2& m) {
 }
 __device__ __forceinline__ f2 exp_neg2(f2 x) { return ex2_2(mul2(x, splat2(-kLog2e))); }
 
+// u = sqrt(v) sig(p_i) x, v = 1 - a^2, the root and the gate each by itself
+__device__ __forceinline__ f2 input_of(f2 v, f2 pi, f2 x) {
+    return mul2(mul2(x, sigmoid2(pi)), mul2(v, f2{rsqrt_approx(v.x), rsqrt_approx(v.y)}));
+}
+__device__ __forceinline__ f2 input2(f2 y, f2 pi, f2 x) {
+    f2 a, m;
+    decay2<true>(y, a, m);
+    return input_of(fma2(m, a, m), pi, x);
+}
 // a and u = sqrt(1 - a^2) sig(p_i) x from y.  With v = 1 - a^2 = m (1 + a) and d = 1 + e^{-p_i},
-// u = x v / sqrt(v d^2): one reciprocal square root for the root and the gate's reciprocal.
-// An infinite d gives u = 0.
-template <bool kWide>
-__device__ __forceinline__ void eval2(f2 y, f2 pi, f2 x, f2& a, f2& u) {
+// u = x v / sqrt(q), q = v d^2: one reciprocal square root for the root and the gate's reciprocal.  Below
+// p_i = -44 q can overflow, and u is 0 then, though x may be large enough to make up for the gate: `over`
+// becomes NaN with a q that is not finite, and the caller takes input2's u for such steps.  That is one packed
+// instruction of about 54: 8x4096x2048 bfloat16 114.9 us, 113.0 without.  (One for two steps, of the product of
+// their q, is no faster: 115.1.)  kApart has no q: its u is input_of's.
+template <bool kWide, bool kApart>
+__device__ __forceinline__ void eval2(f2 y, f2 pi, f2 x, f2& a, f2& u, f2& over) {
     f2 m;
     decay2<kWide>(y, a, m);
     const f2 v = fma2(m, a, m);
-    const f2 d = add2(exp_neg2(pi), splat2(1.0f));
-    const f2 q = mul2(mul2(v, d), d);
-    u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
+    if constexpr (kApart) {
+        u = input_of(v, pi, x);
+    } else {
+        const f2 d = add2(exp_neg2(pi), splat2(1.0f));
+        const f2 q = mul2(mul2(v, d), d);
+        over = fma2(q, splat2(0.0f), over);
+        u = mul2(mul2(x, v), f2{rsqrt_approx(q.x), rsqrt_approx(q.y)});
+    }
 }
 
 template <typename T, bool kTma, bool kCluster, bool kCuts, bool kSum>
@@ -332,6 +349,11 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
     forward_kernel(const Params pr, const __grid_constant__ CUtensorMap map) {
     typedef Tile<T, true, kTma> Tl;
     constexpr int kStages = FwdSmem<T, kTma>::kStages, R = Tl::R, L = Tl::L, kNW = Tl::NW;
+    // Where rows are read from global memory directly, by blocks of their own, the gate has its own reciprocal
+    // (8x2000x2051 float32 110.2 us, with the look at q 114.5); clusters, with a few blocks that wait for
+    // one another, are slower with that (1x100000x63 float32 59.9, 58.4), and so are rings (8x2000x2051
+    // bfloat16 113.1, 107.1).
+    constexpr bool kApart = !kTma && !kHasRing<T, true, kTma> && !kCluster;
     extern __shared__ unsigned char raw[];
     FwdSmem<T, kTma>& sm = *reinterpret_cast<FwdSmem<T, kTma>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, lane = tid & 31;
@@ -453,14 +475,30 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
         if (t0 < T_) {
             // at(j, g): gate g of step j
             auto evaluate = [&](auto at) {
+                f2 over{0.0f, 0.0f};
                 if (!wide) {
 #pragma unroll
                     for (int j = 0; j < R; ++j)
-                        eval2<false>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                        eval2<false, kApart>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j], over);
                 } else {
 #pragma unroll
                     for (int j = 0; j < R; ++j)
-                        eval2<true>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j]);
+                        eval2<true, kApart>(mul2(k, sigmoid2(at(j, 0))), at(j, 1), at(j, 2), a[j], u[j], over);
+                }
+                if (!kApart && ((in0 && over.x != over.x) || (in1 && over.y != over.y))) {
+#pragma unroll 1
+                    for (int j = 0; j < R; ++j) {  // rolled up: this needs no registers of its own
+                        const f2 y = mul2(k, sigmoid2(at(j, 0))), pi = at(j, 1), x = at(j, 2);
+                        f2 aj, uj, own{0.0f, 0.0f};
+                        eval2<true, false>(y, pi, x, aj, uj, own);
+                        const f2 other = input2(y, pi, x);
+                        // only where this step's own q asks for it: a ring has no values for steps past T
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            if (i == j && own.x != own.x) u[i].x = other.x;
+                            if (i == j && own.y != own.y) u[i].y = other.y;
+                        }
+                    }
                 }
             };
             if constexpr (kTma) {

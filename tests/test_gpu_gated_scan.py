@@ -423,3 +423,52 @@ def test_gradient_of_the_input_gate_that_overflows_is_reported(dtype, D):
     with pytest.raises(binding.PararnnError) as e:
         binding.gated_scan_backward(px, lam, ck, dH, DECAY)
     assert e.value.status == binding.ENONFINITE
+
+
+@pytest.mark.parametrize("dtype,D,off", [("f32", 64, 0), ("bf16", 64, 0), ("f32", 33, 0), ("bf16", 33, 0),
+                                         ("f32", 64, 1), ("bf16", 130, 1)])
+def test_gates_next_to_zero_and_large_inputs(dtype, D, off):
+    """p_i down to -86 with x so large that i x is of order 1: the scan, its adjoint and the step agree there"""
+    rng = np.random.default_rng(20)
+    B, T = 2, 150
+    p = np.clip(rng.standard_normal((B, T, 3, D)), -8, 8)
+    p[:, :, 1] = rng.uniform(-86, 8, (B, T, D))
+    px = torch.from_numpy(p).to(TYPES[dtype])
+    px[:, :, 2] = (px[:, :, 2].double() * torch.exp(-px[:, :, 1].double().clamp(max=0))).to(px.dtype)  # to 2^124 N(0, 1)
+    assert torch.isfinite(px).all()
+    px = torch.cat([px.new_zeros(off), px.reshape(-1)]).cuda()[off:].view(px.shape)
+    lam = torch.from_numpy(rng.uniform(-9, 1, D)).float().cuda()
+    dH = torch.from_numpy(rng.standard_normal((B, T, D))).to(TYPES[dtype]).cuda()
+    H, last, ck = binding.gated_scan_forward(px, lam, DECAY, want_grad=True)
+    dpx, dlam, _ = binding.gated_scan_backward(px, lam, ck, dH, DECAY)
+    # the exponential's argument is rounded: U |p| more, 2^-17 for |p| to 86 (and a half step of 2^-126 where a
+    # gate or its product is next to that), so 16 times the bounds for |p| <= 8 holds
+    n = [f64(t) for t in (px, lam, dH)]
+    want, lr = ref.forward(n[0], n[1], DECAY)
+    bound, el = ref.forward_bound(n[0], n[1], DECAY, dtype)
+    within(H, want, 16 * bound, "H")
+    within(last, lr, 16 * el, "h_last")
+    gp, gl, _ = ref.backward(n[0], n[1], DECAY, n[2])
+    ep, ela, _ = ref.backward_bound(n[0], n[1], DECAY, n[2], dtype)
+    within(dpx, gp, 16 * ep + 2.0 ** -126, "dpx")
+    within(dlam, gl, 16 * ela, "dlam")
+    state = torch.zeros(B, D, device="cuda")
+    for t in range(T):
+        y = binding.gated_scan_step(px[:, t].contiguous(), lam, state, DECAY)
+        within(y, want[:, t], 16 * bound[:, t], "step")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bits_do_not_follow_what_earlier_calls_left(dtype):
+    """steps past the end of T, which rows off 16 bytes leave unread: whatever an earlier kernel's shared memory holds"""
+    px, lam, h0, reset, dH, dl = make(2, 500, 33, dtype, True, 25)
+    before = make(40, 1100, 33, dtype, False, 26)[0]
+    got = []
+    for p_i in (0.0, -80.0, float("nan")):
+        before[:, :, 1] = p_i
+        binding.gated_scan_forward(before, lam, DECAY, sync_status=False)
+        H, last, ck = binding.gated_scan_forward(px, lam, DECAY, h0, reset, want_grad=True, sync_status=False)
+        got.append((H, last, ck) + binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True,
+                                                               sync_status=False))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))

@@ -471,9 +471,10 @@ pararnn_status pararnn_head_gru_unroll(int64_t B, int64_t T, int64_t D, int n_he
  *   checkpoints              pararnn_gated_scan_checkpoint_bytes(...) bytes,
  *                            4-byte aligned: states that the backward pass starts
  *                            from, in a layout private to the library; or NULL
- * State, gates and scan are float32.  Apart from h_last and h0, an output that
- * overlaps an input or another output is not supported.  T is at most 2^30, D at
- * most 2^29, B*T below 2^31.
+ * State, gates and scan are float32.  In the scan and its adjoint a sqrt(1 - a^2)
+ * of 0 or next to it comes out up to 5e-19 larger, and |x| beside one below 1e-18 may
+ * not pass 1e20.  Apart from h_last and h0, an output that overlaps an input or
+ * another output is not supported.  T is at most 2^30, D at most 2^29, B*T below 2^31.
  *
  * workspace    NULL, and device-detected conditions are not recorded; or at least
  *              256 bytes, 16-byte aligned, any contents, for

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -71,6 +72,11 @@ struct BwdParams {
 };
 
 __device__ __forceinline__ float softplus_f(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
+// k = c softplus(lambda), so that y = k r; finite for a finite lambda, as 0 k has to be 0
+__device__ __forceinline__ float scale_of(float decay, float lambda) {
+    const float k = decay * softplus_f(lambda);
+    return k > FLT_MAX ? FLT_MAX : k;
+}
 
 // a = e^-y and m = 1 - a for y >= 0.  Below 1/2 m is y times the Taylor series
 // of (1 - e^-y) / y to y^8 (the first omitted term is y^9/10!, below 1e-9 of it) and
@@ -395,8 +401,8 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
     f2 k{0.0f, 0.0f};
-    if (in0) k.x = pr.decay * softplus_f(pr.lam[d]);
-    if (in1) k.y = pr.decay * softplus_f(pr.lam[d + 1]);
+    if (in0) k.x = scale_of(pr.decay, pr.lam[d]);
+    if (in1) k.y = scale_of(pr.decay, pr.lam[d + 1]);
     const bool wide = __any_sync(0xffffffffu, !(k.x <= 1.0f && k.y <= 1.0f));
     if (warp == 0) {
         f2 h{0.0f, 0.0f};
@@ -672,8 +678,10 @@ __device__ __forceinline__ void grads2(f2 y, f2 a, f2 m, f2 l, f2 pi, f2 x, f2 k
     const f2 e = mul2(ib, x);
     const f2 ah = mul2(a, h);
     dx = mul2(l, mul2(v, ib));
-    dpi = mul2(mul2(dx, x), sub2(splat2(1.0f), i));
-    w = mul2(mul2(y, l), sub2(mul2(mul2(a, a), e), ah));
+    // in an order in which no partial product is much larger than its factors and the whole: y may be as large as a
+    // float can be, and a, and with it the difference, is 0 then
+    dpi = mul2(dx, mul2(x, sub2(splat2(1.0f), i)));
+    w = mul2(l, mul2(y, sub2(mul2(mul2(a, a), e), ah)));
     dpr = mul2(w, sub2(splat2(1.0f), mul2(y, kinv)));
     h = fma2(v, e, ah);
 }
@@ -736,8 +744,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
             for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.rank_bar[i], C * (uint32_t)sizeof sm.rank[0][0]);
     }
     f2 k{0.0f, 0.0f};
-    if (in0) k.x = pr.decay * softplus_f(pr.lam[d]);
-    if (in1) k.y = pr.decay * softplus_f(pr.lam[d + 1]);
+    if (in0) k.x = scale_of(pr.decay, pr.lam[d]);
+    if (in1) k.y = scale_of(pr.decay, pr.lam[d + 1]);
     // r = y / k; a k this small gives no gradient to p_r (w is below 2^-60 l)
     const f2 kinv{k.x > 1e-37f ? 1.0f / k.x : 0.0f, k.y > 1e-37f ? 1.0f / k.y : 0.0f};
     const bool wide = __any_sync(0xffffffffu, !(k.x <= 1.0f && k.y <= 1.0f));
@@ -1166,7 +1174,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepParams pr)
     if (!in) return;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) k[i] = pr.decay * softplus_f(k[i]);
+    for (int i = 0; i < V; ++i) k[i] = scale_of(pr.decay, k[i]);
     for (int n = n0;;) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {

@@ -472,3 +472,34 @@ def test_bits_do_not_follow_what_earlier_calls_left(dtype):
                                                                sync_status=False))
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("D", [64, 33])
+@pytest.mark.parametrize("decay,lam,scale", [(1e30, 0.5, 1e10), (3e38, 5.0, 1.0), (8.0, -1.0, 1e20)])
+def test_gradients_overflow_only_where_they_are_large(decay, lam, scale, D):
+    """decays so large that every state is its own step's input, and products of which only a factor overflows"""
+    px, _, _, _, _, _ = make(2, 40, D, "f32", False, 21)
+    px[:, :, 0].clamp_(-2, 2)
+    if decay > 8.0:
+        px[:, 5, 0] = -200.0  # r = 0: the state is kept (|x| beside it is within 1e20)
+    dH = torch.full((2, 40, D), scale, device="cuda")
+    if scale == 1e20:  # x (1 - i) is of order 1, x l is not
+        px[:, :, 1] = 46.0
+        px[:, :, 2] *= 1e20
+        dH[:, :, ::2] = 1e18
+    lam = torch.full((D,), lam, device="cuda")
+    H, last, ck = binding.gated_scan_forward(px, lam, decay, want_grad=True)
+    large = scale == 1e20  # there dL/dp_r, of order l x = 1e38 to 1e40, may be Inf, but nothing is NaN
+    dpx, dlam, _ = binding.gated_scan_backward(px, lam, ck, dH, decay, sync_status=not large)
+    assert torch.isfinite(H).all() and torch.isfinite(dpx[:, :, 1:]).all() and not torch.isnan(dpx).any()
+    if not large:
+        assert torch.isfinite(dpx).all() and torch.isfinite(dlam).all()
+    if decay > 8.0:
+        want = torch.sigmoid(px[:, :, 1].double()) * px[:, :, 2].double()
+        want[:, 5] = want[:, 4]  # a = 1, b = 0
+        assert (H.double() - want).abs().max() <= ref.GATE * want.abs().max()
+        assert (dpx[:, :, 0] == 0).all() and (dlam == 0).all()
+    state = torch.zeros(2, D, device="cuda")
+    for t in range(7):
+        y = binding.gated_scan_step(px[:, t].contiguous(), lam, state, decay)
+        assert (y - H[:, t]).abs().max() <= 4 * ref.GATE * H[:, :7].abs().max()

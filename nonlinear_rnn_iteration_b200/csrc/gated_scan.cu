@@ -1204,8 +1204,11 @@ int64_t n_checkpoints(int64_t T) { return (T + kCkSteps - 1) / kCkSteps; }
 namespace {
 
 // Blocks per cluster: the smallest power of two that fills the device's SMs twice
-// (two blocks are resident per SM), as far as there are tiles for them.
+// (two blocks are resident per SM), as far as there are tiles for them.  Its bound without the
+// device, which has 148 of the kMostSms SMs that the clusters are made for, sizes the workspace.
+constexpr int kMostSms = 256;
 int ranks_for(int64_t groups, int64_t tiles, int sms) {
+    sms = std::min(sms, kMostSms);
     int c = 1;
     while (c < kMaxRanks && c < tiles && groups * c * 2 <= 2 * (int64_t)sms) c *= 2;
     return c;
@@ -1260,14 +1263,20 @@ static_assert(sizeof(BwdSmem<float, true>) + 128 <= kHalfSm && sizeof(BwdSmem<bf
 // Ranges of T: only up to kSegGroups channel groups (which bounds the workspace whatever the device
 // is), as many as bring two blocks to each SM with clusters of 8, of two rounds at least; with
 // fewer than three the second reading costs what the SMs gain.
-constexpr int kSegGroups = 16, kMaxSegs = 32;
+constexpr int kSegGroups = 16, kMaxSegs = 32, kMinSegs = 3;
+int64_t groups_of(int64_t B, int64_t D) { return B * ((D + kW - 1) / kW); }
 size_t elems_bytes(int64_t B, int64_t D) {
-    const int64_t nCG = (D + kW - 1) / kW;
-    return B * nCG <= kSegGroups ? (size_t)(B * nCG * (kMaxSegs + 1)) * 32 * sizeof(float4) : 0;
+    const int64_t groups = groups_of(B, D);
+    return groups <= kSegGroups ? (size_t)(groups * (kMaxSegs + 1)) * 32 * sizeof(float4) : 0;
 }
-size_t part_bytes(int64_t B, int64_t D) {
-    const int64_t segs = elems_bytes(B, D) ? kMaxSegs : 1;
-    return (size_t)(B * D * segs) * kMaxRanks * sizeof(float);
+// The adjoint's partial sums: a row for each block of a channel group, as many as plan() can come to.  (Eight
+// for each would be 2 GB, of which it used 0.3, for 65536 sequences of 32 steps and 1024 channels.)
+size_t part_bytes(int64_t B, int64_t T, int64_t D) {
+    typedef Tile<float, false, false> Tl;  // of L steps for every type
+    const int64_t tiles = (T + Tl::L - 1) / Tl::L;
+    const int ranks = ranks_for(groups_of(B, D), tiles, kMostSms);
+    const bool cut = elems_bytes(B, D) && tiles > (2 * kMinSegs - 1) * kMaxRanks;
+    return (size_t)(B * D * (cut ? kMaxSegs : 1)) * ranks * sizeof(float);
 }
 
 // the grid of either kernel: channel groups, ranges of T, and blocks for each of them
@@ -1282,7 +1291,7 @@ bool plan(P& pr, int L, bool may_cut, int64_t& blocks) {
     int segs = 1;
     if (may_cut && groups <= kSegGroups && pr.ranks == kMaxRanks) {
         segs = (int)std::min<int64_t>(std::min<int64_t>(2 * sms / (groups * pr.ranks), rounds / 2), kMaxSegs);
-        if (segs < 3) segs = 1;
+        if (segs < kMinSegs) segs = 1;
     }
     pr.seg_rounds = (rounds + segs - 1) / segs;
     pr.segs = (rounds + pr.seg_rounds - 1) / pr.seg_rounds;
@@ -1389,7 +1398,8 @@ size_t pararnn_gated_scan_checkpoint_bytes(int64_t B, int64_t T, int64_t D, para
 
 size_t pararnn_gated_scan_workspace_bytes(int64_t B, int64_t T, int64_t D) {
     if (gs::bad_sizes(B, T, D)) return 0;
-    return kHeaderBytes + gs::elems_bytes(B, D) + gs::part_bytes(B, D);
+    if (B == 0 || T == 0 || D == 0) return kHeaderBytes;
+    return kHeaderBytes + gs::elems_bytes(B, D) + gs::part_bytes(B, T, D);
 }
 
 pararnn_status pararnn_gated_scan_forward(int64_t B, int64_t T, int64_t D, pararnn_dtype dtype, const void* preacts,

@@ -150,3 +150,16 @@ def test_reference_norm_matches_torch():
     dx, dw, db = ref.norm_backward(x, dy, w, 1e-3)
     for got, want in ((ref.norm(x, w, b, 1e-3)[0][:, 0], y), (dx[:, 0], tx.grad), (dw[0], tw.grad), (db[0], tb.grad)):
         assert np.abs(got - want.detach().numpy()).max() < 1e-12
+
+
+def test_workspace_follows_the_launch():
+    """a row of partial sums for each block that a channel group can have: no more than tiles of 64 steps, and one
+    where the groups alone fill a device"""
+    ws = binding.pararnn_gated_scan_workspace_bytes
+    row = 65536 * 1024 * 4
+    assert row <= ws(65536, 32, 1024) <= row + 4096
+    assert ws(65536, 64, 1024) == ws(65536, 32, 1024) == ws(65536, 4096, 1024)
+    assert ws(20, 128, 64) - ws(20, 64, 64) == 20 * 64 * 4
+    sizes = [ws(20, T, 64) for T in (1, 64, 65, 129, 300, 520, 4000, 100000)]
+    assert sizes == sorted(sizes) and sizes[-1] == sizes[-2] == 256 + 8 * 20 * 64 * 4
+    assert ws(0, 10, 64) == ws(10, 0, 64) == ws(10, 10, 0) == 256

@@ -503,3 +503,22 @@ def test_gradients_overflow_only_where_they_are_large(decay, lam, scale, D):
     for t in range(7):
         y = binding.gated_scan_step(px[:, t].contiguous(), lam, state, decay)
         assert (y - H[:, t]).abs().max() <= 4 * ref.GATE * H[:, :7].abs().max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 64), (300, 40, 64), (2, 65, 33), (160, 130, 72), (5, 700, 640), (1, 2000, 64),
+                                   (1, 2700, 130), (1, 9000, 24), (17, 3000, 64)])
+def test_backward_stays_in_its_workspace(B, T, D, dtype):
+    """a workspace of exactly the stated size, with a guard behind it, gives what the library's own gives"""
+    px, lam, h0, reset, dH, dl = make(B, T, D, dtype, True, 22)
+    _, _, ck = binding.gated_scan_forward(px, lam, DECAY, h0, reset, want_grad=True)
+    want = binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True)
+    size = binding.pararnn_gated_scan_workspace_bytes(B, T, D)
+    buf = torch.full((size + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = binding.gated_scan_backward(px, lam, ck, dH, DECAY, reset, dl, want_dh0=True, workspace=buf[:size])
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert (buf[size:] == 0xA5).all()
+    H, last, _ = binding.gated_scan_forward(px, lam, DECAY, h0, reset)
+    buf.fill_(0xA5)
+    H2, last2, _ = binding.gated_scan_forward(px, lam, DECAY, h0, reset, workspace=buf[:size])
+    assert torch.equal(H, H2) and torch.equal(last, last2) and (buf[size:] == 0xA5).all()

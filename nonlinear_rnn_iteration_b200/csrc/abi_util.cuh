@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 
@@ -49,6 +50,29 @@ inline pararnn_status open_status(const char* who, void* workspace, size_t ws_by
     if (cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return cuda_fail(who, "workspace reset failed");
     return PARARNN_OK;
 }
+// A kernel's attributes are set once per device; `done` holds a bit per device.
+template <class Kern>
+bool prepare_kernel(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
+inline int sm_count() {
+    static thread_local int dev_of = -1, sms = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev != dev_of) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        dev_of = dev;
+    }
+    return sms;
+}
+
 // A launch that may begin while the stream's previous kernel is still running, if
 // that kernel allows it (follow_previous): the blocks wait for its end, and for its memory to be
 // visible, before they touch global memory, so only the launch itself overlaps.

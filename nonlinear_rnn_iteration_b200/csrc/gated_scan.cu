@@ -1214,34 +1214,11 @@ int ranks_for(int64_t groups, int64_t tiles, int sms) {
     return c;
 }
 
-// A kernel's attributes are set once per device; `done` holds a bit per device.
-template <class Kern>
-bool prepare_kernel(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (done.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
-    done.fetch_or(bit, std::memory_order_release);
-    return true;
-}
-
-int sm_count() {
-    static thread_local int dev_of = -1, sms = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev != dev_of) {
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        dev_of = dev;
-    }
-    return sms;
-}
-
 template <auto kern, int kThreadCount, class P, class Map>
 pararnn_status launch_clusters(const char* who, const P& pr, const Map& map, int64_t blocks, int ranks,
                                size_t smem, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    if (!prepare_kernel(kern, smem, done)) return abi::cuda_fail(who, "kernel attributes not accepted");
+    if (!abi::prepare_kernel(kern, smem, done)) return abi::cuda_fail(who, "kernel attributes not accepted");
     return abi::launch(who, kern, dim3((unsigned)blocks), kThreadCount, smem, st, ranks, pr, map);
 }
 
@@ -1282,7 +1259,7 @@ size_t part_bytes(int64_t B, int64_t T, int64_t D) {
 // the grid of either kernel: channel groups, ranges of T, and blocks for each of them
 template <class P>
 bool plan(P& pr, int L, bool may_cut, int64_t& blocks) {
-    const int sms = sm_count();
+    const int sms = abi::sm_count();
     pr.nCG = (int)((pr.D + kW - 1) / kW);
     pr.nCk = (int)n_checkpoints(pr.T);
     const int64_t groups = pr.B * pr.nCG, tiles = (pr.T + L - 1) / L;

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -811,17 +812,6 @@ void with_shape(const Plan& p, F f) {
 #undef PARARNN_LN
 }
 
-int sm_count() {
-    static thread_local int dev_of = -1, sms = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev != dev_of) {
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        dev_of = dev;
-    }
-    return sms;
-}
-
 // Blocks: as many as are resident at `threads_per_sm` threads per SM, or as there are rows
 // for; `slots` ranges of positions for each range of parameter rows.
 int64_t slots_for(const Plan& p, int64_t M, int sms, int threads_per_sm) {
@@ -831,7 +821,7 @@ int64_t slots_for(const Plan& p, int64_t M, int sms, int threads_per_sm) {
 
 template <typename T>
 pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
-    const int sms = sm_count();
+    const int sms = abi::sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
     const bool by16 = (pr.N * sizeof(T)) % 16 == 0 && !abi::misaligned(pr.x, 16) && !abi::misaligned(pr.y, 16);
     const bool by4 = (pr.N * sizeof(T)) % 4 == 0 && !abi::misaligned(pr.x, 4) && !abi::misaligned(pr.y, 4);
@@ -847,17 +837,20 @@ pararnn_status launch_forward(const char* who, Params pr, cudaStream_t st) {
         constexpr int V = decltype(v)::value, K = decltype(k)::value, most = decltype(big)::value;
         auto kern = forward_rows<T, V, K, most>;
         constexpr int words = words_of<T, V, K>;
-        const size_t smem = (p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0) +
-                            (kRing<T, V, K, most, true> ? (size_t)p.threads * words * batch_of(words) * 4 : 0);
-        if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        s = abi::launch(who, kern, dim3((unsigned)blocks), p.threads, smem, st, 1, pr);
+        constexpr size_t ring = kRing<T, V, K, most, true> ? (size_t)most * words * batch_of(words) * 4 : 0;
+        const size_t smem = (p.each > 16 ? (size_t)p.tpr * p.each * 2 * sizeof(float) : 0) + ring;
+        constexpr size_t largest = (V * K > 16 ? (size_t)most * V * K * 2 * sizeof(float) : 0) + ring;
+        static std::atomic<uint64_t> done{0};
+        s = abi::prepare_kernel(kern, largest, done)
+                ? abi::launch(who, kern, dim3((unsigned)blocks), p.threads, smem, st, 1, pr)
+                : abi::cuda_fail(who, "kernel attributes not accepted");
     });
     return s;
 }
 
 template <typename T>
 pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* db, cudaStream_t st) {
-    const int sms = sm_count();
+    const int sms = abi::sm_count();
     if (sms <= 0) return abi::cuda_fail(who, "device query failed");
     const int64_t C = pr.P * pr.N;
     const bool sums = dw || db;
@@ -883,11 +876,15 @@ pararnn_status launch_backward(const char* who, BwdParams pr, float* dw, float* 
         with_shape<T, false>(p, [&](auto v, auto k, auto big) {
             constexpr int V = decltype(v)::value, K = decltype(k)::value, most = decltype(big)::value;
             auto kern = backward_rows<T, V, K, most>;
-            const size_t ring = kRing<T, V, K, most, false>
-                                    ? (size_t)p.threads * words_of<T, V, K> * kBackRows<T, V, K, most> * 8
-                                    : 0;
-            const size_t smem = std::max(sums ? (size_t)V * K * p.threads * sizeof(float2) : 0, ring);
-            if (smem > 47 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            constexpr size_t ring =
+                kRing<T, V, K, most, false> ? (size_t)most * words_of<T, V, K> * kBackRows<T, V, K, most> * 8 : 0;
+            constexpr size_t columns = (size_t)V * K * most * sizeof(float2);
+            const size_t smem = sums ? std::max(columns, ring) : ring;
+            static std::atomic<uint64_t> done{0};
+            if (!abi::prepare_kernel(kern, std::max(columns, ring), done)) {
+                s = abi::cuda_fail(who, "kernel attributes not accepted");
+                return;
+            }
             s = abi::launch(who, kern, dim3((unsigned)(parts * p.npc)), p.threads, smem, st, 1, pr);
         });
     }

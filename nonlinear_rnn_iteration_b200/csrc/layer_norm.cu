@@ -58,9 +58,12 @@ struct BwdParams {
 // shares a block barrier between them.  Two reductions of a row in the forward pass
 // (the variance is taken about the mean), one of two sums in the backward pass.
 // Batches in which every thread of the block has all its values take a copy of the code without
-// conditions (100000x1x256 bfloat16 27 and 43 us, 29 and 45 without), where its registers allow that:
-// with 64 values a thread forward (32768x3x2048 163 us, 152 without the copy) and 16 backward
-// (283, 248 without) it spills.
+// conditions where that was measured to gain (replayed from a graph, with and without): in the forward with
+// vector accesses and 256 threads of up to 32 values (100000x1x256 bfloat16 20.1 us, 23.5; 131072x1x1024
+// float32 184, 190) and in the backward with up to 8 values (100000x1x256 37.4, 41.1).  Not with the larger blocks of
+// longer rows (8x1x8192 bfloat16 11.3, 10.6; 16384x1x16384 float32 374, 354), with single values
+// (20000x1x1001 float32 53.4, 50.9), nor with 64 values forward (32768x3x2048 bfloat16 163, 152) or 16
+// backward (283, 248).  What the compiler reports as spilled does not follow these gains.
 // Measured: 131072x1x1024 float32 188 us forward, 5.7 TB/s, and 250 us backward, 6.4 TB/s, bound by HBM;
 // 32768x3x2048 bfloat16 152 us, 5.3 TB/s, bound by the latency of the row loads, for which
 // registers are left, and 249 us, 4.9 TB/s, bound by issue and the rows' barrier; rows of 64, 32768x8x64
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) forward_row
         }
     };
     for (uint32_t it = 0; it < rows.steps; it += U) {
-        if constexpr (E <= 32)
+        if constexpr (kThreads == 256 && V > 1 && E <= 32)
             it + U <= rows.full ? batch(it, std::true_type{}) : batch(it, std::false_type{});
         else
             batch(it, std::false_type{});

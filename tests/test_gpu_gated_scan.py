@@ -522,3 +522,53 @@ def test_backward_stays_in_its_workspace(B, T, D, dtype):
     buf.fill_(0xA5)
     H2, last2, _ = binding.gated_scan_forward(px, lam, DECAY, h0, reset, workspace=buf[:size])
     assert torch.equal(H, H2) and torch.equal(last, last2) and (buf[size:] == 0xA5).all()
+
+
+def test_decoding_steps_in_a_graph():
+    """one captured step replayed per token, its inputs refilled between: the states that the scan gives"""
+    px, lam, h0, _, _, _ = make(3, 30, 136, "bf16", False, 23)
+    state = torch.zeros(7, 136, device="cuda")
+    slots = torch.tensor([6, -1, 1, 4], dtype=torch.int32, device="cuda")
+    state[slots[[0, 2, 3]].long()] = h0
+    row = torch.zeros(4, 3, 136, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((4, 136), 5.0, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.gated_scan_step(row, lam, state, DECAY, slots, out=y, sync_status=False)
+    want, lr = ref.forward(f64(px), f64(lam), DECAY, f64(h0))
+    bound, el = ref.forward_bound(f64(px), f64(lam), DECAY, "bf16", f64(h0))
+    for t in range(30):
+        row[[0, 2, 3]] = px[:, t]
+        graph.replay()
+        within(y[[0, 2, 3]], want[:, t], bound[:, t], "y")
+    assert (y[1] == 5.0).all()
+    within(state[slots[[0, 2, 3]].long()], lr, el, "state")
+
+
+def test_overlapped_launches_beside_the_newton_solver():
+    """calls whose launches overlap the end of the kernel before them, between cluster forwards of the Newton solver
+    on one stream and each on the other's output: the bits of the same calls with the GPU idle between them"""
+    B, T, D = 2, 1024, 64
+    px, lam, _, _, dH, _ = make(B, T, D, "f32", False, 24)
+    diag = torch.full((3, D), 0.5, device="cuda")
+
+    def run(wait):
+        out, x = [], px
+        for _ in range(4):
+            H = binding.newton_forward("diag_gru", x, diag, K=3, sync_status=False)[:, :, 0].contiguous()
+            wait()
+            z, _, _ = binding.layer_norm_forward(H, sync_status=False)
+            wait()
+            x = x + z.unsqueeze(2) * 0.1
+            H2, _, ck = binding.gated_scan_forward(x, lam, DECAY, want_grad=True, sync_status=False)
+            wait()
+            dpx, dlam, _ = binding.gated_scan_backward(x, lam, ck, dH, DECAY, sync_status=False)
+            wait()
+            x = dpx.contiguous()
+            out += [H, z, H2, dpx, dlam]
+        torch.cuda.synchronize()
+        return out
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, run(lambda: None)))

@@ -458,7 +458,9 @@ pararnn_status pararnn_head_gru_unroll(int64_t B, int64_t T, int64_t D, int n_he
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,     h_{-1} = h0.
  * A step that `reset` marks starts from a zero state: h_t has no term in
  * h_{t-1}, whatever h_{t-1} is, a NaN or Inf included.  Marking the first steps
- * of sequences laid one behind the other keeps them apart.
+ * of sequences laid one behind the other keeps them apart.  The input of a marked
+ * step is scaled by sqrt(1 - a^2) like every other's; published cells of this form
+ * take a sequence's first input unscaled.
  *
  * Layouts (row-major, channels fastest, device memory owned by the caller):
  *   preacts    (B, T, 3, D)  dtype (float32 or bfloat16): p_r, p_i, x
@@ -526,6 +528,8 @@ pararnn_status pararnn_gated_scan_backward(int64_t B, int64_t T, int64_t D, para
  *   preacts  (N, 3, D) dtype;  y (N, D) dtype, written
  *   slots    (N) int32, or NULL for slot n of row n (N <= n_slots)
  *   state    (n_slots, D) float32, read and written
+ * There is no mark here: a sequence that begins on a used slot wants that row of
+ * `state` set to zero first.
  * A row whose slot is negative is padding: its y is left as it was.  Rows that
  * name the same slot are taken in the order of their rows, each on the state that
  * the one before left.  A slot at or above n_slots is an error that the GPU

@@ -130,11 +130,11 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // buffers are not multiples of 16 bytes (kTma false) each warp copies the 16-byte granules that
 // hold its rows' pieces (RowRing), or reads them directly.
 //
-// Measured: 4x32768x1024 float32 347 us, 6.2 TB/s, bound by HBM; bfloat16, which has half the bytes
-// for the same arithmetic, 8x4096x2048 118 us, 4.6 TB/s, and 1x131072x4096 in clusters 955 us, 4.5 TB/s,
+// Measured: 4x32768x1024 float32 320 us, 6.7 TB/s (with checkpoints 367), bound by HBM; bfloat16, which has
+// half the bytes for the same arithmetic, 8x4096x2048 115 us, 4.7 TB/s, and 1x131072x4096 in clusters 955 us, 4.5 TB/s,
 // bound by instructions, the special-function unit and the tile's phases, which overlap only between
-// the two blocks of an SM.  16 steps a thread halve what a tile costs beside its steps (1x131072x4096:
-// 928 us; with 12, 996, and with 8, 1140).
+// the two blocks of an SM.  16 steps a thread halve what a tile costs beside its steps (1x131072x4096, at
+// an earlier build: 1.07 times its time with 12, 1.23 with 8).
 constexpr int kW = 64;  // channels per block
 constexpr int kMaxRanks = 8;
 
@@ -172,9 +172,9 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
 // them a round (its steps' gates), each the 16-byte granules that hold 64 channels,
 // brought by one bulk copy of one lane.  A round with a piece whose granules reach over the ends
 // of its array is marked and read from global memory directly.  8x2000x2051 bfloat16: forward
-// 107 us, with direct loads alone 146, as two 2-byte loads stand for one of 4; adjoint 213, 268.
-// float32: adjoint of 16x1000x1001 150 us, direct 159, but forward 67.6, direct 65.5, so that pass
-// has no ring.
+// 109 us, adjoint 212; float32 adjoint of 16x1000x1001 146 us.  At an earlier build: the former 107 and 213,
+// with direct loads alone 146 and 268, as two 2-byte loads stand for one of 4; the latter 150, direct 159, but the
+// float32 forward 67.6, direct 65.5, so that pass has no ring.
 template <typename T, int kN>
 struct RowRing {
     static constexpr int kSlots = sizeof(T) == 2 ? 2 : 1, kPitch = kW * (int)sizeof(T) + 16;
@@ -645,14 +645,16 @@ __global__ void __launch_bounds__(Tile<T, true, kTma>::NW * 32, 2)
 // first step, for h_{t-1} and the gradients: of the states one in R is read, and the
 // forward's scan is not repeated.
 //
-// Measured: 4x32768x1024 float32 613 us, 6.1 TB/s, bound by HBM; bfloat16 8x4096x2048 181 us, 5.2 TB/s,
-// 1x131072x4096 in clusters 1.60 ms, 4.7 TB/s, bound as the forward is.
+// Measured: 4x32768x1024 float32 614 us, 6.1 TB/s, bound by HBM; bfloat16 8x4096x2048 176 us, 5.3 TB/s,
+// 1x131072x4096 in clusters 1.59 ms, 4.7 TB/s, bound as the forward is.  With marks on 1 step in 500 674 us, 196 us and
+// 2.06 ms.  The instance for float32 rows off 16 bytes in clusters spills 100 bytes, with marks 176, the
+// aligned one with marks 16; the others up to 4.
 template <typename T, bool kTma>
 struct BwdSmem {
     static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? 2 : 0;  // stages of p_r and g, of p_i and x
     static constexpr int kRows = kTma ? Tile<T, false, kTma>::L : 1;
-    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time (8x4096x2048: 180 us,
-    // against 190 with the threads' own stores of two channels); float32 has no room for it
+    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time (8x4096x2048, at an
+    // earlier build: 180 us, 190 with the threads' own stores of two channels); float32 has no room for it
     static constexpr bool kOut = kTma && sizeof(T) == 2;
     alignas(128) T pr[kA + !kTma][kRows][kW];
     alignas(128) T g[kA + !kTma][kRows][kW];
@@ -777,8 +779,8 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
 
     constexpr bool kOut = BwdSmem<T, kTma>::kOut;
     // bfloat16, which waits for instructions and latency, reads the checkpoint and the warps'
-    // elements ahead (8x4096x2048: 181 us, against 210 without); float32, which waits for HBM, has no registers for that
-    // (4x32768x1024: 650 us with, 613 without)
+    // elements ahead (8x4096x2048, at an earlier build: 181 us, 210 without); float32, which waits for HBM, has no
+    // registers for that (4x32768x1024: 650 us with, 613 without)
     constexpr bool kEarly = sizeof(T) == 2;
     // pieces 4 j .. 4 j + 3: the gates and dL/dH of step j
     auto piece = [&](int t, int j, int g) {
@@ -1093,8 +1095,8 @@ struct StepParams {
 // few rows and by HBM for many.  Rows that name the same slot must be taken in order:
 // the block of the first of them takes them all, each with the state that the one before left,
 // and the others' blocks end.  Every block looks through the slots for that, N
-// words that the L2 cache holds, while its own loads are on their way.  Measured with its launch:
-// 250x2048 float32 10 us, 1500x2048 bfloat16 23 us (18 without slots to look through).
+// words that the L2 cache holds, while its own loads are on their way.  Replayed from a graph:
+// 1x4096 bfloat16 2.8 us, 250x2048 float32 4.9, 1500x2048 bfloat16 16.7 (12.4 without slots to look through).
 constexpr int kStepThreads = 256;
 constexpr int kStepRows = 8192;  // rows of one launch
 

@@ -64,11 +64,10 @@ struct BwdParams {
 // longer rows (8x1x8192 bfloat16 11.3, 10.6; 16384x1x16384 float32 374, 354), with single values
 // (20000x1x1001 float32 53.4, 50.9), nor with 64 values forward (32768x3x2048 bfloat16 163, 152) or 16
 // backward (283, 248).  What the compiler reports as spilled does not follow these gains.
-// Measured: 131072x1x1024 float32 188 us forward, 5.7 TB/s, and 250 us backward, 6.4 TB/s, bound by HBM;
-// 32768x3x2048 bfloat16 152 us, 5.3 TB/s, bound by the latency of the row loads, for which
+// Measured: 131072x1x1024 float32 186 us forward, 5.8 TB/s, and 245 us backward, 6.6 TB/s, bound by HBM;
+// 32768x3x2048 bfloat16 149 us, 5.4 TB/s, bound by the latency of the row loads, for which
 // registers are left, and 249 us, 4.9 TB/s, bound by issue and the rows' barrier; rows of 64, 32768x8x64
-// bfloat16, 21 us and 33 us, bound by instructions (places kept as running sums and a reciprocal
-// root of few instructions took the forward from 27 to 22).
+// bfloat16, 15 us and 28 us, bound by instructions.
 template <typename T, int V, int K>
 constexpr int words_of = K * (V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1);
 constexpr int batch_of(int words) { return words >= 16 ? 1 : words >= 8 ? 2 : 4; }
@@ -256,11 +255,11 @@ struct NoRing {
     __device__ __forceinline__ NoRing(unsigned char*, uint64_t*) {}
 };
 // Where rows are brought ahead: with 16-byte accesses, and where a row has a warp at least (more
-// than 8 values a thread).  In the backward pass (131072x1x1024 float32 251 us, 279 without;
-// 32768x3x2048 bfloat16 249, 253), but not with 1024 threads, whose 64 registers spill (16384x1x16384
-// float32 1435 us, 1250 without).  In the forward only with 512 threads, one block to an SM
-// (16384x1x16384 float32 377, 454 without); more blocks hide the loads themselves, and the rings
-// take their shared memory (32768x3x2048 bfloat16 164, 152 without).
+// than 8 values a thread).  Measured at earlier builds, with and without: in the backward pass (131072x1x1024
+// float32 251 us, 279; 32768x3x2048 bfloat16 249, 253), but not with 1024 threads, whose 64 registers spill
+// (16384x1x16384 float32 1435 us, 1250).  In the forward only with 512 threads, one block to an SM
+// (16384x1x16384 float32 377, 454); more blocks hide the loads themselves, and the rings
+// take their shared memory (32768x3x2048 bfloat16 164, 152).
 template <typename T, int V, int K, int kThreads, bool kForward>
 constexpr bool kRing = V * sizeof(T) == 16 && V * K > 8 && (kForward ? kThreads == 512 : kThreads <= 512);
 // rows that a thread of the backward pass reads at a time
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     const float n = (float)N, inv = 1.0f / n;
     int turn = 0;
     // with 1024 threads, of 64 registers, the column sums stay in shared memory (16384x1x16384 float32
-    // 1112 us, in spilled registers 1287)
+    // 1110 us; in spilled registers, at an earlier build, 1287)
     f2 w[E / 2], dw[kHold ? E / 2 : 1], db[kHold ? E / 2 : 1], chk{0.0f, 0.0f};
     auto params = [&]() {
 #pragma unroll
@@ -618,7 +617,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
 
 // ---- rows of any length -----------------------------------------------------------
 // For rows that do not fit a block's registers: a block per row, which reads it
-// once for each sum; the column sums are formed by a kernel of their own.
+// once for each sum; the column sums are formed by a kernel of their own.  4096x1x20000 bfloat16 207 us
+// forward, 460 backward (the bytes of one reading and writing at the copy's rate: 50 and 75), float32 237 and 584
+// (100 and 150): values are loaded one at a time, and each input three times.
 constexpr int kLongThreads = 512;
 
 __device__ __forceinline__ float2 block_sum(float a, float b) {
@@ -763,10 +764,10 @@ int pow2_at_least(int64_t n) {
 }
 
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
-// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16: 152 us with
-// 64 values and a warp per row, 270 with 8 and a block); past 8192 columns, where the weights in
-// shared memory leave one block to an SM, 32 and so 512 threads (16384x1x16384 bfloat16 272 us,
-// 437 with 64 and 256 threads).  With few rows the smaller count leaves more threads to each of
+// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16, at earlier builds:
+// 152 us with 64 values and a warp per row, 270 with 8 and a block); past 8192 columns, where the weights in
+// shared memory leave one block to an SM, 32 and so 512 threads (16384x1x16384 bfloat16 270 us; 437
+// with 64 and 256 threads).  With few rows the smaller count leaves more threads to each of
 // them.  The backward pass, which holds two column sums for each value, has 8, or 16 past 256
 // columns (32768x3x2048 bfloat16: 249 us with 16, 289 with 8).  A row of 256 bytes or more needs no
 // neighbours: the block's rows then share one parameter row.

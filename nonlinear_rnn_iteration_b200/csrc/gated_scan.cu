@@ -133,8 +133,8 @@ __device__ __forceinline__ Row gates(float pr, float pi, float x, float k) {
 // Measured: 4x32768x1024 float32 320 us, 6.7 TB/s (with checkpoints 367), bound by HBM; bfloat16, which has
 // half the bytes for the same arithmetic, 8x4096x2048 115 us, 4.7 TB/s, and 1x131072x4096 in clusters 955 us, 4.5 TB/s,
 // bound by instructions, the special-function unit and the tile's phases, which overlap only between
-// the two blocks of an SM.  16 steps a thread halve what a tile costs beside its steps (1x131072x4096, at
-// an earlier build: 1.07 times its time with 12, 1.23 with 8).
+// the two blocks of an SM.  16 steps a thread halve what a tile costs beside its steps (1x131072x4096, on
+// earlier code: 1.07 times its time with 12, 1.23 with 8).
 constexpr int kW = 64;  // channels per block
 constexpr int kMaxRanks = 8;
 
@@ -172,7 +172,7 @@ __device__ __forceinline__ Elem then(const Elem& e, const Elem& f) {
 // them a round (its steps' gates), each the 16-byte granules that hold 64 channels,
 // brought by one bulk copy of one lane.  A round with a piece whose granules reach over the ends
 // of its array is marked and read from global memory directly.  8x2000x2051 bfloat16: forward
-// 109 us, adjoint 212; float32 adjoint of 16x1000x1001 146 us.  At an earlier build: the former 107 and 213,
+// 109 us, adjoint 212; float32 adjoint of 16x1000x1001 146 us.  On earlier code: the former 107 and 213,
 // with direct loads alone 146 and 268, as two 2-byte loads stand for one of 4; the latter 150, direct 159, but the
 // float32 forward 67.6, direct 65.5, so that pass has no ring.
 template <typename T, int kN>
@@ -653,8 +653,8 @@ template <typename T, bool kTma>
 struct BwdSmem {
     static constexpr int kA = kTma ? 4 / sizeof(T) : 0, kB = kTma ? 2 : 0;  // stages of p_r and g, of p_i and x
     static constexpr int kRows = kTma ? Tile<T, false, kTma>::L : 1;
-    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time (8x4096x2048, at an
-    // earlier build: 180 us, 190 with the threads' own stores of two channels); float32 has no room for it
+    // the gradients of bfloat16 leave by tensor copies, a warp's steps at a time (8x4096x2048, on
+    // earlier code: 180 us, 190 with the threads' own stores of two channels); float32 has no room for it
     static constexpr bool kOut = kTma && sizeof(T) == 2;
     alignas(128) T pr[kA + !kTma][kRows][kW];
     alignas(128) T g[kA + !kTma][kRows][kW];
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(Tile<T, false, kTma>::NW * 32, 2)
 
     constexpr bool kOut = BwdSmem<T, kTma>::kOut;
     // bfloat16, which waits for instructions and latency, reads the checkpoint and the warps'
-    // elements ahead (8x4096x2048, at an earlier build: 181 us, 210 without); float32, which waits for HBM, has no
+    // elements ahead (8x4096x2048, on earlier code: 181 us, 210 without); float32, which waits for HBM, has no
     // registers for that (4x32768x1024: 650 us with, 613 without)
     constexpr bool kEarly = sizeof(T) == 2;
     // pieces 4 j .. 4 j + 3: the gates and dL/dH of step j

@@ -255,7 +255,7 @@ struct NoRing {
     __device__ __forceinline__ NoRing(unsigned char*, uint64_t*) {}
 };
 // Where rows are brought ahead: with 16-byte accesses, and where a row has a warp at least (more
-// than 8 values a thread).  Measured at earlier builds, with and without: in the backward pass (131072x1x1024
+// than 8 values a thread).  Measured on earlier code, with and without: in the backward pass (131072x1x1024
 // float32 251 us, 279; 32768x3x2048 bfloat16 249, 253), but not with 1024 threads, whose 64 registers spill
 // (16384x1x16384 float32 1435 us, 1250).  In the forward only with 512 threads, one block to an SM
 // (16384x1x16384 float32 377, 454); more blocks hide the loads themselves, and the rings
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) backward_ro
     const float n = (float)N, inv = 1.0f / n;
     int turn = 0;
     // with 1024 threads, of 64 registers, the column sums stay in shared memory (16384x1x16384 float32
-    // 1110 us; in spilled registers, at an earlier build, 1287)
+    // 1110 us; in spilled registers, on earlier code, 1287)
     f2 w[E / 2], dw[kHold ? E / 2 : 1], db[kHold ? E / 2 : 1], chk{0.0f, 0.0f};
     auto params = [&]() {
 #pragma unroll
@@ -764,7 +764,7 @@ int pow2_at_least(int64_t n) {
 }
 
 // Values per thread: as many as a warp needs to hold the row, 8 to 64 of bfloat16 and 8 to 32
-// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16, at earlier builds:
+// of float32, so that short and middle rows need no block barrier (32768x3x2048 bfloat16, on earlier code:
 // 152 us with 64 values and a warp per row, 270 with 8 and a block); past 8192 columns, where the weights in
 // shared memory leave one block to an SM, 32 and so 512 threads (16384x1x16384 bfloat16 270 us; 437
 // with 64 and 256 threads).  With few rows the smaller count leaves more threads to each of
